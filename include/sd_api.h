@@ -312,6 +312,128 @@ sd_status sd_indexer_topk_noalloc(const int8_t* qi, const int32_t* w, const int8
                                   sd_paged_desc pd, int32_t B, int32_t Hi, int32_t Di,
                                   int32_t max_seqlen, int32_t k, int32_t* indices, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A blocked cache: one layer's paged K and V, [num_pages, page_size, kv_heads,
+ * D] each, with a page cut into blocks of `block_tokens` slots (block_tokens
+ * divides page_size). kv_type is the pools' element type. An 8-bit pool has
+ * one fp32 scale per (block, KV head): the value of a code is code * scale.
+ * k_bounds holds the smallest and the largest key of every block, KV head and
+ * dim, for the selection of blocks; it may be NULL where nothing is selected.
+ * Its entries, like the scales, stand for the tokens that the block holds.
+ * D in {64, 128}, block_tokens <= 128, num_pages * page_size and
+ * max_pages_per_req * page_size < 2^31; pools and bounds 16-byte aligned
+ * (SD_ERR_INVALID_ARG otherwise). (No counterpart on the pages: they read
+ * caches that a serving stack has written.) */
+typedef enum sd_kv_type { SD_KV_BF16 = 0, SD_KV_INT8 = 1, SD_KV_E4M3 = 2 } sd_kv_type;
+
+typedef struct sd_kv_cache {
+  void* k_pages;      /* [num_pages, page_size, G, D] of kv_type                     */
+  void* v_pages;      /* the same                                                    */
+  float* k_scales;    /* [num_pages, page_size / block_tokens, G]; 8-bit pools only  */
+  float* v_scales;    /* the same                                                    */
+  uint16_t* k_bounds; /* bf16 [num_pages, page_size / block_tokens, G, 2, D], or NULL */
+  int32_t kv_type;    /* sd_kv_type                                                  */
+  int32_t block_tokens;
+  int32_t D;
+} sd_kv_cache;
+
+/* Norm, rotation and store of new tokens, one launch. The new tokens of request b
+ * are rows tok_start[b] .. tok_start[b + 1] - 1 of q, k and v; they become the
+ * last positions of the request, seqlens[b] - n .. seqlens[b] - 1 (seqlens
+ * counts them). One row per request is a decode step; more are a prompt or a
+ * chunk of one. A request may have none.
+ *   q, k, v     bf16 rows [n_tokens][H or G heads][D], heads dense, rows
+ *               q_stride, k_stride, v_stride elements apart (a packed q, k, v
+ *               projection is read in place); 8-byte aligned, strides
+ *               multiples of 4. q may be NULL (only K and V are stored)
+ *   tok_start   int32 [B + 1], ascending from 0; rows at or behind
+ *               tok_start[B] are not read, and their q_out rows stay as they were
+ *   positions   int32 [n_tokens]: the position each row is rotated to, or NULL:
+ *               its position in the cache
+ *   q_weight, k_weight  bf16 [D] or NULL (no norm): x * rsqrt(mean(x^2) + eps) * weight
+ *               over each head
+ *   inv_freq    fp32 [rot_dim / 2]: angle of pair i = position * inv_freq[i].
+ *               The first rot_dim dims rotate (a multiple of 8, at most D; 0:
+ *               none, inv_freq may be NULL), in pairs (i, i + rot_dim / 2), or
+ *               (2i, 2i + 1) with interleaved != 0
+ *   q_out       bf16 [n_tokens, H, D], 8-byte aligned; may be q where q is dense
+ * Arithmetic is fp32, angles fp64; q_out and bf16 pools are rounded once. In
+ * an 8-bit pool the scale of a (block, KV head) is
+ *   max(amax(new rows) / qmax, the scale it had if it holds earlier tokens, 2^-100)
+ * (qmax 127 or 448), codes are round(y / scale), and earlier codes of a block
+ * whose scale grew are coded anew, round(code * old / new). NaN is stored as
+ * code 0 and an infinity as the largest code; neither enters the scale.
+ * k_bounds of a block are those of its tokens' bf16 keys. Pool rows, scales and bounds
+ * of other blocks are not touched; two requests must not share a block that
+ * either writes. A bad block-table entry flags SD_DEVERR_PAGE and that
+ * block's rows are not stored; more rows than seqlens[b] flags
+ * SD_DEVERR_INDEX and the rows before position 0 are not stored. */
+sd_status sd_kv_store(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, const int32_t* tok_start, const int32_t* positions,
+                      const int32_t* block_table, const int32_t* seqlens, sd_paged_desc pd, sd_kv_cache kv, int32_t B,
+                      int32_t n_tokens, int32_t H, const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                      const float* inv_freq, int32_t rot_dim, int32_t interleaved, uint16_t* q_out, void* stream);
+
+/* Reads the tokens that sd_kv_store with the same tok_start and seqlens stores
+ * back as bf16 rows (for example the cached prefix of a prompt, for an
+ * attention over bf16 rows): the last n tokens of every request.
+ *   k_out, v_out  bf16 [n_tokens, G, D], 16-byte aligned: code * scale, rounded once.
+ * Rows at or behind tok_start[B] stay as they were; a token whose page is bad
+ * or whose position is negative reads as zeros and is flagged. */
+sd_status sd_kv_load(sd_kv_cache kv, const int32_t* tok_start, const int32_t* block_table, const int32_t* seqlens,
+                     sd_paged_desc pd, int32_t B, int32_t n_tokens, uint16_t* k_out, uint16_t* v_out, void* stream);
+
+/* Decode attention over an 8-bit blocked cache, one query per request:
+ *   z_j = scale * sk_j * (q . k_j), out = sum_j softmax_j(z) * sv_j * v_j
+ * over every cached token (indices NULL), or over listed blocks.
+ *   q        bf16 [B, H, D], 16-byte aligned
+ *   indices  int32 [B, G, n_list]: entry e selects the tokens e * index_block ..
+ *            of the request (1: tokens, as sd_indexer_topk writes them; the
+ *            blocks of sd_block_topk: its block_tokens). Only the first
+ *            min(n_list, ceil(seqlen / index_block)) entries of a row are read; entries < 0 are
+ *            skipped, one that starts at or past the seqlen is skipped and
+ *            flags SD_DEVERR_INDEX, tokens past the seqlen are dropped,
+ *            duplicates are attended as listed
+ *   out      bf16 [B, H, D], 8-byte aligned; zero where nothing is attended
+ *   lse      fp32 [B, H] or NULL: ln sum exp z, -inf where nothing is attended
+ * H % G == 0, H / G <= 128, n_list * index_block < 2^30. Scales must be finite
+ * and not negative. A token on a bad page is skipped and flags SD_DEVERR_PAGE.
+ * Slots behind a request's last token may hold anything.
+ * kv_type SD_KV_BF16 returns SD_ERR_UNSUPPORTED (sd_sparse_attn reads bf16 pools).
+ * Workspace: sd_kv_attn_workspace_size(). */
+size_t sd_kv_attn_workspace_size(int32_t B, int32_t G, int32_t H, int32_t D);
+sd_status sd_kv_attn(const uint16_t* q, sd_kv_cache kv, const int32_t* block_table, const int32_t* seqlens,
+                     const int32_t* indices, int32_t n_list, int32_t index_block, sd_paged_desc pd, int32_t B,
+                     int32_t H, float scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* Selection of blocks by a bound on their scores (any kv_type; kv.k_bounds is
+ * read, the pools are not): block c of KV head g scores
+ *   max over the group's query heads of sum_d max(q_d * lo_d, q_d * hi_d)
+ * summed in fp64 and rounded to fp32, at least the largest q . k of the block.
+ *   indices  int32 [B, G, n_select]  OUT: the first n_first and the last n_last
+ *            blocks of the request and the best others, min(n_select, number
+ *            of blocks) together, ties to the lower block; ascending, -1 padded
+ * 1 <= n_select <= 2048, n_first + n_last <= n_select, max_seqlen <= 2^20 *
+ * block_tokens, B * G <= 65535, H / G <= 128. A block on a bad page scores -inf and
+ * flags SD_DEVERR_PAGE. max_seqlen is a host upper bound of seqlens.
+ * The indices fit sd_kv_attn with index_block = block_tokens, and
+ * sd_sparse_attn_csr with offsets r * n_select and block_size = block_tokens.
+ * Workspace: sd_block_topk_workspace_size(). */
+size_t sd_block_topk_workspace_size(int32_t B, int32_t G, int32_t max_seqlen, int32_t block_tokens);
+sd_status sd_block_topk(const uint16_t* q, sd_kv_cache kv, const int32_t* block_table, const int32_t* seqlens,
+                        sd_paged_desc pd, int32_t B, int32_t H, int32_t max_seqlen, int32_t n_select, int32_t n_first,
+                        int32_t n_last, int32_t* indices, void* workspace, size_t workspace_bytes, void* stream);
+
+/* sd_block_topk and sd_kv_attn over the blocks it selects, in one call
+ * (arguments and errors as above). Workspace: sd_kv_block_step_workspace_size(). */
+size_t sd_kv_block_step_workspace_size(int32_t B, int32_t G, int32_t H, int32_t D, int32_t max_seqlen,
+                                       int32_t block_tokens);
+sd_status sd_kv_block_step(const uint16_t* q, sd_kv_cache kv, const int32_t* block_table, const int32_t* seqlens,
+                           sd_paged_desc pd, int32_t B, int32_t H, int32_t max_seqlen, int32_t n_select,
+                           int32_t n_first, int32_t n_last, float scale, int32_t* indices, uint16_t* out, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 /* Stage timing for monitoring and benchmarks (no counterpart on the pages).
  * `events` points to 2 * n cudaEvent_t handles created by the caller; while
  * set, every call of this thread records events[2*i] just before and

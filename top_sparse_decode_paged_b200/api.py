@@ -27,12 +27,19 @@ EXPORTED = ("sd_workspace_size", "sd_indexer_topk", "sd_indexer_topk_noalloc", "
             "sd_sparse_attn_csr", "sd_indexer_topk_hinted", "sd_decode_step_hinted", "sd_decode_step",
             "sd_tri_workspace_size", "sd_tri_compact", "sd_tri_layers_workspace_size", "sd_tri_compact_layers",
             "sd_set_stage_events", "sd_set_wait_limit", "sd_get_device_errors", "sd_status_str", "sd_last_cuda_error",
-            "sd_last_launch_count", "sd_version")
+            "sd_last_launch_count", "sd_version", "sd_kv_store", "sd_kv_load", "sd_kv_attn_workspace_size", "sd_kv_attn",
+            "sd_block_topk_workspace_size", "sd_block_topk", "sd_kv_block_step_workspace_size", "sd_kv_block_step")
 
 
 class PagedDesc(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("max_pages_per_req", ctypes.c_int32), ("kv_heads", ctypes.c_int32)]
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_bounds", ctypes.c_void_p), ("kv_type", ctypes.c_int32),
+                ("block_tokens", ctypes.c_int32), ("D", ctypes.c_int32)]
 
 
 class SdError(RuntimeError):
@@ -95,6 +102,24 @@ def load_library(path: Optional[str] = None):
     lib.sd_tri_compact_layers.restype = i32
     lib.sd_tri_compact_layers.argtypes = [p, p, p, i32, p, p, PagedDesc, i32, i32, i32, i32, i32, i32, i32, i32, p, p,
                                           sz, p]
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.sd_kv_store.restype = i32
+    lib.sd_kv_store.argtypes = [p, p, p, i64, i64, i64, p, p, p, p, PagedDesc, KvDesc, i32, i32, i32, p, p, f32, p, i32,
+                                i32, p, p]
+    lib.sd_kv_load.restype = i32
+    lib.sd_kv_load.argtypes = [KvDesc, p, p, p, PagedDesc, i32, i32, p, p, p]
+    lib.sd_kv_attn_workspace_size.restype = sz
+    lib.sd_kv_attn_workspace_size.argtypes = [i32] * 4
+    lib.sd_kv_attn.restype = i32
+    lib.sd_kv_attn.argtypes = [p, KvDesc, p, p, p, i32, i32, PagedDesc, i32, i32, f32, p, p, p, sz, p]
+    lib.sd_block_topk_workspace_size.restype = sz
+    lib.sd_block_topk_workspace_size.argtypes = [i32] * 4
+    lib.sd_block_topk.restype = i32
+    lib.sd_block_topk.argtypes = [p, KvDesc, p, p, PagedDesc, i32, i32, i32, i32, i32, i32, p, p, sz, p]
+    lib.sd_kv_block_step_workspace_size.restype = sz
+    lib.sd_kv_block_step_workspace_size.argtypes = [i32] * 6
+    lib.sd_kv_block_step.restype = i32
+    lib.sd_kv_block_step.argtypes = [p, KvDesc, p, p, PagedDesc, i32, i32, i32, i32, i32, i32, f32, p, p, p, p, sz, p]
     lib.sd_set_stage_events.restype = i32
     lib.sd_set_stage_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), i32]
     lib.sd_set_wait_limit.restype = i32
@@ -390,6 +415,242 @@ def sd_tri_compact_layers(q_cals, k_pools, v_pools, block_table, seqlens, max_se
                                      int(max_seqlen), int(n_sink), int(n_recent), int(budget), int(mode),
                                      _ptr(new_seqlens), _ptr(workspace), workspace.numel(), _stream(stream)))
     return new_seqlens
+
+
+SD_KV_BF16 = 0
+SD_KV_INT8 = 1
+SD_KV_E4M3 = 2
+_KV_TYPES = {torch.bfloat16: SD_KV_BF16, torch.int8: SD_KV_INT8, torch.float8_e4m3fn: SD_KV_E4M3}
+
+
+def _need(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+    """The data pointer of a contiguous tensor of that type, shape and device."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on {device}")
+    return t.data_ptr()
+
+
+class KvCache:
+    """One layer's blocked cache: paged K and V pools ``[num_pages, page_size,
+    G, D]`` (bf16, int8 or float8_e4m3fn) cut into blocks of ``block_tokens``
+    slots, fp32 scales ``[num_pages, page_size // block_tokens, G]`` of 8-bit
+    pools and, where blocks are selected, the bf16 bounds of every block's
+    keys ``[num_pages, page_size // block_tokens, G, 2, D]`` (lo, hi). Holds
+    the tensors; the library reads and writes them in place."""
+
+    def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None, k_bounds=None, block_tokens: Optional[int] = None):
+        if k_pages.dim() != 4 or k_pages.dtype not in _KV_TYPES:
+            raise ValueError("k_pages must be bf16, int8 or float8_e4m3fn [num_pages, page_size, G, D]")
+        N, P, G, D = k_pages.shape
+        bs = P if block_tokens is None else int(block_tokens)
+        if bs < 1 or P % bs != 0:
+            raise ValueError(f"block_tokens {bs} does not divide the page size {P}")
+        self.device = k_pages.device
+        if self.device.type != "cuda":
+            raise ValueError("tensors passed to the library must be on the GPU")
+        self.num_pages, self.page_size, self.G, self.D, self.block_tokens = N, P, G, D, bs
+        self.kv_type = _KV_TYPES[k_pages.dtype]
+        kp = _need(k_pages, "k_pages", k_pages.dtype, (N, P, G, D), self.device)
+        vp = _need(v_pages, "v_pages", k_pages.dtype, (N, P, G, D), self.device)
+        ks = vs = kb = None
+        if self.kv_type != SD_KV_BF16:
+            if k_scales is None or v_scales is None:
+                raise ValueError("8-bit pools need k_scales and v_scales")
+            ks = _need(k_scales, "k_scales", torch.float32, (N, P // bs, G), self.device)
+            vs = _need(v_scales, "v_scales", torch.float32, (N, P // bs, G), self.device)
+        if k_bounds is not None:
+            kb = _need(k_bounds, "k_bounds", torch.bfloat16, (N, P // bs, G, 2, D), self.device)
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales, self.k_bounds = k_pages, v_pages, k_scales, v_scales, k_bounds
+        self._kv = KvDesc(kp, vp, ks, vs, kb, self.kv_type, bs, D)
+
+    def _paged(self, block_table, B: int):
+        if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
+                block_table.device != self.device or not block_table.is_contiguous():
+            raise ValueError(f"block_table must be contiguous int32 [{B}, pages] on {self.device}")
+        return block_table.data_ptr(), PagedDesc(self.num_pages, self.page_size, block_table.shape[1], self.G)
+
+    def _call(self, stream, fn, *args):
+        """Enqueues on ``stream`` or the cache's device's current one, with that device current."""
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        if torch.cuda.current_device() == self.device.index:
+            _check(fn(*args, s.cuda_stream))
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(*args, s.cuda_stream))
+
+    def _empty(self, shape, dtype, stream):
+        """A new tensor whose memory belongs to the stream the call runs on."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def alloc_kv_cache(num_pages: int, page_size: int, G: int, D: int, dtype=torch.int8, block_tokens: Optional[int] = None,
+                   bounds: bool = True, device=None) -> KvCache:
+    """An empty blocked cache (all zeros)."""
+    device = device or "cuda"
+    nb = page_size // (block_tokens or page_size)
+    pools = [torch.zeros((num_pages, page_size, G, D), dtype=torch.uint8 if dtype != torch.bfloat16 else dtype,
+                         device=device) for _ in range(2)]
+    k, v = [x if dtype == torch.bfloat16 else x.view(dtype) for x in pools]
+    ks = vs = None
+    if dtype != torch.bfloat16:
+        ks, vs = (torch.zeros((num_pages, nb, G), dtype=torch.float32, device=device) for _ in range(2))
+    kb = torch.zeros((num_pages, nb, G, 2, D), dtype=torch.bfloat16, device=device) if bounds else None
+    return KvCache(k, v, ks, vs, kb, block_tokens)
+
+
+def _rows(t, name: str, T: int, heads: int, cache: KvCache):
+    """Pointer and row stride of token rows [T, heads, D] whose heads are dense."""
+    D = cache.D
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, heads, D) or t.device != cache.device:
+        raise ValueError(f"{name}: expected bf16 {(T, heads, D)} on {cache.device}, got {t.dtype} {tuple(t.shape)}")
+    st = t.stride()
+    if T > 0 and (st[2] != 1 or (heads > 1 and st[1] != D)):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    return t.data_ptr(), st[0] if T > 1 else heads * D
+
+
+def sd_kv_store(q, k, v, cache: KvCache, block_table, seqlens, tok_start, inv_freq, q_weight=None, k_weight=None,
+                eps: float = 1e-6, interleaved: bool = False, positions=None, q_out=None, stream=None):
+    """Norm and rotation of the new tokens' queries and keys, and the store of
+    K and V as the last positions of their requests. ``q`` [T, H, D] (or None),
+    ``k``, ``v`` [T, G, D] may be views into a packed projection; request b's
+    rows are ``tok_start[b]:tok_start[b + 1]``. ``inv_freq`` is fp32
+    [rot_dim / 2] or None. Returns ``q_out`` [T, H, D] bf16 (None without q)."""
+    B, T = seqlens.shape[0], k.shape[0]
+    G, D, dev = cache.G, cache.D, cache.device
+    kp, ks = _rows(k, "k", T, G, cache)
+    vp, vs = _rows(v, "v", T, G, cache)
+    qp, qs, H, qo = None, 0, 0, None
+    if q is not None:
+        H = q.shape[1]
+        qp, qs = _rows(q, "q", T, H, cache)
+        if q_out is None:
+            q_out = cache._empty((T, H, D), torch.bfloat16, stream)
+        qo = _need(q_out, "q_out", torch.bfloat16, (T, H, D), dev)
+    bt, pd = cache._paged(block_table, B)
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    cache._call(stream, load_library().sd_kv_store, qp, kp, vp, qs, ks, vs,
+                _need(tok_start, "tok_start", torch.int32, (B + 1,), dev),
+                None if positions is None else _need(positions, "positions", torch.int32, (T,), dev), bt,
+                _need(seqlens, "seqlens", torch.int32, (B,), dev), pd, cache._kv, B, T, H,
+                None if q_weight is None else _need(q_weight, "q_weight", torch.bfloat16, (D,), dev),
+                None if k_weight is None else _need(k_weight, "k_weight", torch.bfloat16, (D,), dev), eps,
+                None if inv_freq is None else _need(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev), rot,
+                1 if interleaved else 0, qo)
+    return q_out
+
+
+def sd_kv_load(cache: KvCache, block_table, seqlens, tok_start, n_tokens: int, k_out=None, v_out=None, stream=None):
+    """The tokens that ``sd_kv_store`` with the same arguments stores, read
+    back as bf16. Returns ``(k_out, v_out)`` [n_tokens, G, D]; rows behind
+    ``tok_start[B]`` are left as they are."""
+    B, dev, shape = seqlens.shape[0], cache.device, (n_tokens, cache.G, cache.D)
+    if k_out is None:
+        k_out = cache._empty(shape, torch.bfloat16, stream)
+    if v_out is None:
+        v_out = cache._empty(shape, torch.bfloat16, stream)
+    bt, pd = cache._paged(block_table, B)
+    cache._call(stream, load_library().sd_kv_load, cache._kv, _need(tok_start, "tok_start", torch.int32, (B + 1,), dev),
+                bt, _need(seqlens, "seqlens", torch.int32, (B,), dev), pd, B, n_tokens,
+                _need(k_out, "k_out", torch.bfloat16, shape, dev), _need(v_out, "v_out", torch.bfloat16, shape, dev))
+    return k_out, v_out
+
+
+def alloc_kv_attn_workspace(B: int, G: int, H: int, D: int, device=None) -> torch.Tensor:
+    """Scratch for ``sd_kv_attn`` (torch's allocator returns 256-byte aligned blocks)."""
+    n = int(load_library().sd_kv_attn_workspace_size(B, G, H, D))
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device or "cuda")
+
+
+def alloc_block_topk_workspace(B: int, G: int, max_seqlen: int, block_tokens: int, device=None) -> torch.Tensor:
+    """Scratch for ``sd_block_topk``."""
+    n = int(load_library().sd_block_topk_workspace_size(B, G, max_seqlen, block_tokens))
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device or "cuda")
+
+
+def alloc_block_step_workspace(B: int, G: int, H: int, D: int, max_seqlen: int, block_tokens: int,
+                               device=None) -> torch.Tensor:
+    """Scratch for ``sd_kv_block_step``."""
+    n = int(load_library().sd_kv_block_step_workspace_size(B, G, H, D, max_seqlen, block_tokens))
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device or "cuda")
+
+
+def _workspace(workspace, nbytes: int, cache: KvCache, stream):
+    if workspace is None:
+        workspace = cache._empty((max(nbytes, 1),), torch.uint8, stream)
+    if workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {cache.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def sd_kv_attn(q, cache: KvCache, block_table, seqlens, scale: float, indices=None, index_block: int = 1, out=None,
+               lse=None, workspace=None, stream=None):
+    """Attention of one query per request over an 8-bit cache: every cached
+    token, or the blocks of ``index_block`` tokens that ``indices`` [B, G, n]
+    lists (1: tokens). Returns ``out`` [B, H, D] bf16."""
+    lib = load_library()
+    B, H = q.shape[0], q.shape[1]
+    G, D, dev = cache.G, cache.D, cache.device
+    if out is None:
+        out = cache._empty((B, H, D), torch.bfloat16, stream)
+    n, ip = 0, None
+    if indices is not None:
+        n = indices.shape[-1]
+        ip = _need(indices, "indices", torch.int32, (B, G, n), dev)
+    ws, ws_bytes = _workspace(workspace, 0 if workspace is not None else lib.sd_kv_attn_workspace_size(B, G, H, D), cache,
+                              stream)
+    bt, pd = cache._paged(block_table, B)
+    cache._call(stream, lib.sd_kv_attn, _need(q, "q", torch.bfloat16, (B, H, D), dev), cache._kv, bt,
+                _need(seqlens, "seqlens", torch.int32, (B,), dev), ip, n, index_block, pd, B, H, scale,
+                _need(out, "out", torch.bfloat16, (B, H, D), dev),
+                None if lse is None else _need(lse, "lse", torch.float32, (B, H), dev), ws, ws_bytes)
+    return out
+
+
+def sd_block_topk(q, cache: KvCache, block_table, seqlens, n_select: int, max_seqlen: int, n_first: int = 1,
+                  n_last: int = 1, indices=None, workspace=None, stream=None):
+    """The blocks of each (request, KV head) with the largest bound on their
+    scores, the first ``n_first`` and last ``n_last`` always among them.
+    Returns ``indices`` [B, G, n_select] int32, ascending, -1 padded."""
+    lib = load_library()
+    B, H = q.shape[0], q.shape[1]
+    G, D, dev = cache.G, cache.D, cache.device
+    if indices is None:
+        indices = cache._empty((B, G, n_select), torch.int32, stream)
+    ws, ws_bytes = _workspace(workspace, 0 if workspace is not None else
+                              lib.sd_block_topk_workspace_size(B, G, max_seqlen, cache.block_tokens), cache, stream)
+    bt, pd = cache._paged(block_table, B)
+    cache._call(stream, lib.sd_block_topk, _need(q, "q", torch.bfloat16, (B, H, D), dev), cache._kv, bt,
+                _need(seqlens, "seqlens", torch.int32, (B,), dev), pd, B, H, max_seqlen, n_select, n_first, n_last,
+                _need(indices, "indices", torch.int32, (B, G, n_select), dev), ws, ws_bytes)
+    return indices
+
+
+def sd_kv_block_step(q, cache: KvCache, block_table, seqlens, n_select: int, max_seqlen: int, scale: float,
+                     n_first: int = 1, n_last: int = 1, indices=None, out=None, lse=None, workspace=None, stream=None):
+    """``sd_block_topk``, then ``sd_kv_attn`` over the blocks it selects.
+    Returns (indices [B, G, n_select] int32, out [B, H, D] bf16)."""
+    lib = load_library()
+    B, H = q.shape[0], q.shape[1]
+    G, D, dev = cache.G, cache.D, cache.device
+    if indices is None:
+        indices = cache._empty((B, G, n_select), torch.int32, stream)
+    if out is None:
+        out = cache._empty((B, H, D), torch.bfloat16, stream)
+    ws, ws_bytes = _workspace(workspace, 0 if workspace is not None else
+                              lib.sd_kv_block_step_workspace_size(B, G, H, D, max_seqlen, cache.block_tokens), cache, stream)
+    bt, pd = cache._paged(block_table, B)
+    cache._call(stream, lib.sd_kv_block_step, _need(q, "q", torch.bfloat16, (B, H, D), dev), cache._kv, bt,
+                _need(seqlens, "seqlens", torch.int32, (B,), dev), pd, B, H, max_seqlen, n_select, n_first, n_last, scale,
+                _need(indices, "indices", torch.int32, (B, G, n_select), dev),
+                _need(out, "out", torch.bfloat16, (B, H, D), dev),
+                None if lse is None else _need(lse, "lse", torch.float32, (B, H), dev), ws, ws_bytes)
+    return indices, out
 
 
 def set_wait_limit(polls: int) -> None:

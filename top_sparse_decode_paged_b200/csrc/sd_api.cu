@@ -14,8 +14,11 @@
 #include "../../include/sd_api.h"
 #include "attn_mma.cuh"
 #include "attn_umma.cuh"
+#include "block_topk.cuh"
 #include "indexer_dp4a.cuh"
 #include "indexer_umma.cuh"
+#include "kv_attn.cuh"
+#include "kv_store.cuh"
 #include "sd_common.cuh"
 #include "sparse_index.cuh"
 #include "topk_cluster.cuh"
@@ -898,7 +901,7 @@ int64_t sd_probe_read(void* dst, int64_t max_bytes) {
 
 int32_t sd_last_cuda_error(void) { return t_last_cuda_error; }
 int32_t sd_last_launch_count(void) { return t_launches; }
-int32_t sd_version(void) { return (0 << 16) | 7; }
+int32_t sd_version(void) { return (0 << 16) | 8; }
 
 }  // extern "C"
 
@@ -960,3 +963,363 @@ extern "C" sd_status sd_indexer_topk_noalloc(const int8_t* qi, const int32_t* w,
   return launch_indexer_topk(qi, w, ki_pages, block_table, seqlens, pd, B, Hi, Di, max_seqlen, k,
                              indices, scores, static_cast<cudaStream_t>(stream));
 }
+
+// ---------------------------------------------------------------------------
+// The blocked cache: norm + rotation + store, read-back, attention over 8-bit
+// pools, selection of blocks by their bounds.
+// ---------------------------------------------------------------------------
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+sd_status check_cache(const sd_kv_cache& kv, const sd_paged_desc& pd) {
+  if (!geom_ok(pd) || !kv.k_pages || !kv.v_pages || kv.D <= 0 || kv.block_tokens <= 0) return SD_ERR_INVALID_ARG;
+  if (kv.kv_type != SD_KV_BF16 && kv.kv_type != SD_KV_INT8 && kv.kv_type != SD_KV_E4M3) return SD_ERR_INVALID_ARG;
+  if (kv.kv_type != SD_KV_BF16 && (!kv.k_scales || !kv.v_scales)) return SD_ERR_INVALID_ARG;
+  if (pd.page_size % kv.block_tokens != 0) return SD_ERR_INVALID_ARG;
+  if (!aligned(kv.k_pages, 16) || !aligned(kv.v_pages, 16) || !aligned(kv.k_bounds, 16) || !aligned(kv.k_scales, 4) ||
+      !aligned(kv.v_scales, 4))
+    return SD_ERR_INVALID_ARG;
+  if ((kv.D != 64 && kv.D != 128) || kv.block_tokens > sd::kKvMaxBlock) return SD_ERR_UNSUPPORTED;
+  if ((long long)pd.num_pages * pd.page_size >= (1ll << 31) || (long long)pd.max_pages_per_req * pd.page_size >= (1ll << 31))
+    return SD_ERR_UNSUPPORTED;
+  return SD_OK;
+}
+
+sd::KvGeom kv_geom(const sd_kv_cache& kv, const sd_paged_desc& pd) {
+  sd::KvGeom g;
+  g.num_pages = pd.num_pages;
+  g.page_size = pd.page_size;
+  g.max_pages = pd.max_pages_per_req;
+  g.G = pd.kv_heads;
+  g.bs = kv.block_tokens;
+  g.blocks_per_page = pd.page_size / kv.block_tokens;
+  g.page_div = sd::make_fast_div(pd.page_size);
+  g.bs_div = sd::make_fast_div(kv.block_tokens);
+  return g;
+}
+
+// How the attention over 8-bit pools is cut up: a function of the shape only.
+struct KvAttnPlan {
+  int nt, cols, col_groups, spw, ranges;
+  size_t off_ml, total;
+};
+KvAttnPlan kv_attn_plan(int B, int G, int H, int D) {
+  KvAttnPlan p{};
+  const int qpk = H / G;
+  p.nt = qpk > 8 ? 2 : 1;  // 16 query heads share a warp's unpacked K and V above 8 per KV head
+  p.cols = G * sd::ceil_div(qpk, 8 * p.nt);
+  p.col_groups = sd::ceil_div(p.cols, sd::kKaWarps);
+  p.spw = p.cols >= sd::kKaWarps ? 1 : sd::kKaWarps / p.cols;
+  p.ranges = std::max(1, sd::kKaRanges / (p.nt == 2 ? 2 : 1) / p.col_groups);
+  const size_t rows = ((size_t)p.ranges + B) * p.spw * H;
+  p.off_ml = align_up(rows * D * sizeof(float));
+  p.total = p.off_ml + align_up(rows * sizeof(float2));
+  return p;
+}
+
+sd_status check_kv_attn_args(const uint16_t* q, const sd_kv_cache& kv, const int32_t* bt, const int32_t* seqlens,
+                             const sd_paged_desc& pd, int B, int H, float scale, const uint16_t* out) {
+  const sd_status s = check_cache(kv, pd);
+  if (s != SD_OK) return s;
+  if (B < 0 || H <= 0 || H % pd.kv_heads != 0 || !isfinite(scale)) return SD_ERR_INVALID_ARG;
+  if (B > 0 && (!q || !bt || !seqlens || !out || !aligned(q, 16) || !aligned(out, 8))) return SD_ERR_INVALID_ARG;
+  if (kv.kv_type == SD_KV_BF16 || H / pd.kv_heads > 128 || (long long)B * H >= (1ll << 31)) return SD_ERR_UNSUPPORTED;
+  return SD_OK;
+}
+
+template <int D, int NT, int TYPE, bool LIST>
+sd_status launch_kv_attn_t(const sd::KvAttnArgs& a, cudaStream_t st) {
+  auto kern = sd::kv_attn_kernel<D, NT, TYPE, LIST>;
+  constexpr size_t smem = sd::KvAttnCfg<D, NT>::kSmem;
+  const sd_status s = set_smem_limit(reinterpret_cast<const void*>(kern), smem);
+  if (s != SD_OK) return s;
+  return launch_k(kern, dim3(a.ranges, a.col_groups), dim3(sd::kKaThreads), smem, st, a);
+}
+
+sd_status launch_kv_attn(const uint16_t* q, const sd_kv_cache& kv, const int32_t* bt, const int32_t* seqlens,
+                         const int32_t* indices, int n_list, int index_block, const sd_paged_desc& pd, int B, int H,
+                         float scale, int cap, uint16_t* out, float* lse, void* ws, cudaStream_t st) {
+  const int G = pd.kv_heads;
+  const KvAttnPlan p = kv_attn_plan(B, G, H, kv.D);
+  sd::KvAttnArgs a{};
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.k_pages = static_cast<const uint8_t*>(kv.k_pages);
+  a.v_pages = static_cast<const uint8_t*>(kv.v_pages);
+  a.k_scales = kv.k_scales;
+  a.v_scales = kv.v_scales;
+  a.block_table = bt;
+  a.seqlens = seqlens;
+  a.indices = indices;
+  a.geo = kv_geom(kv, pd);
+  a.B = B;
+  a.H = H;
+  a.qpk = H / G;
+  a.n_list = n_list;
+  a.index_block = index_block;
+  a.index_div = sd::make_fast_div(index_block);
+  a.cap = cap;
+  a.cols = p.cols;
+  a.col_groups = p.col_groups;
+  a.spw = p.spw;
+  a.ranges = p.ranges;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.part_o = static_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  sd_status s = SD_OK;
+  stage_mark(kStageAttn, 0, st);
+#define SD_KA(D_, NT_)                                                                                        \
+  s = kv.kv_type == SD_KV_INT8 ? (indices ? launch_kv_attn_t<D_, NT_, SD_KV_INT8, true>(a, st)                \
+                                          : launch_kv_attn_t<D_, NT_, SD_KV_INT8, false>(a, st))              \
+                               : (indices ? launch_kv_attn_t<D_, NT_, SD_KV_E4M3, true>(a, st)                \
+                                          : launch_kv_attn_t<D_, NT_, SD_KV_E4M3, false>(a, st))
+  if (kv.D == 64) {
+    if (p.nt == 1) SD_KA(64, 1); else SD_KA(64, 2);
+  } else {
+    if (p.nt == 1) SD_KA(128, 1); else SD_KA(128, 2);
+  }
+#undef SD_KA
+  stage_mark(kStageAttn, 1, st);
+  if (s != SD_OK) return s;
+  stage_mark(kStageCombine, 0, st);
+  s = launch_k(kv.D == 64 ? sd::kv_attn_combine_kernel<64> : sd::kv_attn_combine_kernel<128>, dim3(B * H),
+               dim3(sd::kKaCombineThreads), 0, st, a);
+  stage_mark(kStageCombine, 1, st);
+  return s;
+}
+
+// Keys and counts of the block selection inside its workspace.
+size_t block_keys_bytes(int B, int G, int max_blocks) {
+  return align_up(sizeof(int32_t) * (size_t)B * G * std::max(max_blocks, 1));
+}
+
+sd_status check_block_topk_args(const uint16_t* q, const sd_kv_cache& kv, const int32_t* bt, const int32_t* seqlens,
+                                const sd_paged_desc& pd, int B, int H, int max_seqlen, int n_select, int n_first,
+                                int n_last, const int32_t* indices) {
+  const sd_status s = check_cache(kv, pd);
+  if (s != SD_OK) return s;
+  if (!kv.k_bounds || B < 0 || H <= 0 || H % pd.kv_heads != 0 || max_seqlen < 0 || n_select <= 0 || n_first < 0 ||
+      n_last < 0 || (long long)n_first + n_last > n_select)
+    return SD_ERR_INVALID_ARG;
+  if (B > 0 && (!q || !bt || !seqlens || !indices)) return SD_ERR_INVALID_ARG;
+  if (n_select > kMaxK || H / pd.kv_heads > 128 || (long long)B * pd.kv_heads > 65535 ||
+      (max_seqlen + (long long)kv.block_tokens - 1) / kv.block_tokens > kMaxSeqlen)
+    return SD_ERR_UNSUPPORTED;
+  return SD_OK;
+}
+
+template <int D>
+sd_status launch_block_score(const sd::BlockScoreArgs& a, cudaStream_t st) {
+  constexpr size_t smem = sd::BlockScoreCfg<D>::kSmem;
+  const sd_status s = set_smem_limit(reinterpret_cast<const void*>(sd::block_score_kernel<D>), smem);
+  if (s != SD_OK) return s;
+  const dim3 grid(std::max(1, sd::ceil_div(a.max_blocks, sd::kBtBlocks * sd::kBtWarps)), a.B * a.geo.G);
+  return launch_k(sd::block_score_kernel<D>, grid, dim3(sd::kBtThreads), smem, st, a);
+}
+
+sd_status launch_block_topk(const uint16_t* q, const sd_kv_cache& kv, const int32_t* bt, const int32_t* seqlens,
+                            const sd_paged_desc& pd, int B, int H, int max_seqlen, int n_select, int n_first,
+                            int n_last, int32_t* indices, void* ws, cudaStream_t st) {
+  const int G = pd.kv_heads;
+  const int max_blocks = static_cast<int>((max_seqlen + (long long)kv.block_tokens - 1) / kv.block_tokens);
+  sd::BlockScoreArgs a{};
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.bounds = reinterpret_cast<const __nv_bfloat16*>(kv.k_bounds);
+  a.block_table = bt;
+  a.seqlens = seqlens;
+  a.geo = kv_geom(kv, pd);
+  a.B = B;
+  a.H = H;
+  a.qpk = H / G;
+  a.max_blocks = max_blocks;
+  a.cap = std::min(max_seqlen, pd.max_pages_per_req * pd.page_size);
+  a.n_first = n_first;
+  a.n_last = n_last;
+  a.keys = static_cast<int32_t*>(ws);
+  a.counts = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + block_keys_bytes(B, G, max_blocks));
+  stage_mark(kStageIndexer, 0, st);
+  const sd_status s = kv.D == 64 ? launch_block_score<64>(a, st) : launch_block_score<128>(a, st);
+  stage_mark(kStageIndexer, 1, st);
+  if (s != SD_OK) return s;
+  return launch_topk(a.keys, a.counts, indices, B, G, max_blocks, max_blocks, n_select, sd::RowMap{}, nullptr, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+sd_status sd_kv_store(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, const int32_t* tok_start, const int32_t* positions,
+                      const int32_t* block_table, const int32_t* seqlens, sd_paged_desc pd, sd_kv_cache kv, int32_t B,
+                      int32_t n_tokens, int32_t H, const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                      const float* inv_freq, int32_t rot_dim, int32_t interleaved, uint16_t* q_out, void* stream) {
+  t_launches = 0;
+  sd_status s = check_cache(kv, pd);
+  if (s != SD_OK) return s;
+  const int G = pd.kv_heads;
+  if (B < 0 || n_tokens < 0 || (q && (H <= 0 || !q_out)) || !isfinite(eps) || eps < 0.f || rot_dim < 0 || rot_dim > kv.D ||
+      rot_dim % 8 != 0 || (rot_dim > 0 && !inv_freq))
+    return SD_ERR_INVALID_ARG;
+  if (B > 0 && n_tokens > 0) {
+    if (!k || !v || !tok_start || !block_table || !seqlens) return SD_ERR_INVALID_ARG;
+    // rows are read 4 elements (8 bytes) at a time
+    if (!aligned(q, 8) || !aligned(k, 8) || !aligned(v, 8) || !aligned(q_out, 8) || !aligned(q_weight, 8) ||
+        !aligned(k_weight, 8) || (k_stride | v_stride) % 4 != 0 || (q && q_stride % 4 != 0) ||
+        (q && q_stride < (int64_t)H * kv.D) || k_stride < (int64_t)G * kv.D || v_stride < (int64_t)G * kv.D)
+      return SD_ERR_INVALID_ARG;
+  }
+  const bool full = rot_dim == kv.D && !interleaved;
+  sd::KvStoreArgs a{};
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  a.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.tok_start = tok_start;
+  a.positions = positions;
+  a.block_table = block_table;
+  a.seqlens = seqlens;
+  a.geo = kv_geom(kv, pd);
+  a.k_pages = kv.k_pages;
+  a.v_pages = kv.v_pages;
+  a.k_scales = kv.k_scales;
+  a.v_scales = kv.v_scales;
+  a.bounds = reinterpret_cast<__nv_bfloat16*>(kv.k_bounds);
+  a.kv_type = kv.kv_type;
+  a.B = B;
+  a.T = n_tokens;
+  a.H = q ? H : 0;
+  a.cap = pd.max_pages_per_req * pd.page_size;
+  a.qw = reinterpret_cast<const __nv_bfloat16*>(q_weight);
+  a.kw = reinterpret_cast<const __nv_bfloat16*>(k_weight);
+  a.eps = eps;
+  a.inv_freq = inv_freq;
+  a.R = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
+  // a request touches at most n / block_tokens + 2 blocks; where that does not
+  // beat one unit per row, rows are the units and need no search over requests
+  const long long touched = n_tokens / kv.block_tokens + 2ll * B;
+  a.by_row = n_tokens <= touched;
+  const long long kv_ctas = std::min<long long>(n_tokens, touched) * G;
+  // heads per lane group: as many as leave two waves of groups
+  const int groups = sd::kKvThreads / (kv.D / 8);
+  a.heads_per_group = std::max(1, std::min(a.H, 32));
+  while (a.heads_per_group > sd::kKvQHeads &&
+         (long long)n_tokens * sd::ceil_div(a.H, a.heads_per_group) < 2ll * 148 * groups)
+    a.heads_per_group = (a.heads_per_group + 1) / 2;
+  a.head_groups = sd::ceil_div(a.H, a.heads_per_group);
+  const long long q_ctas = ((long long)n_tokens * a.head_groups + groups - 1) / groups;
+  if (kv_ctas + q_ctas >= (1ll << 31)) return SD_ERR_UNSUPPORTED;
+  if (B == 0 || n_tokens == 0) return SD_OK;
+  a.kv_ctas = static_cast<int>(kv_ctas);
+  auto kern = kv.D == 64 ? (full ? sd::kv_store_kernel<64, true> : sd::kv_store_kernel<64, false>)
+                         : (full ? sd::kv_store_kernel<128, true> : sd::kv_store_kernel<128, false>);
+  return launch_k(kern, dim3(static_cast<unsigned>(kv_ctas + q_ctas)), dim3(sd::kKvThreads), 0,
+                  static_cast<cudaStream_t>(stream), a);
+}
+
+sd_status sd_kv_load(sd_kv_cache kv, const int32_t* tok_start, const int32_t* block_table, const int32_t* seqlens,
+                     sd_paged_desc pd, int32_t B, int32_t n_tokens, uint16_t* k_out, uint16_t* v_out, void* stream) {
+  t_launches = 0;
+  const sd_status s = check_cache(kv, pd);
+  if (s != SD_OK) return s;
+  if (B < 0 || n_tokens < 0) return SD_ERR_INVALID_ARG;
+  if (B == 0 || n_tokens == 0) return SD_OK;
+  if (!tok_start || !block_table || !seqlens || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return SD_ERR_INVALID_ARG;
+  sd::KvLoadArgs a{};
+  a.k_pages = kv.k_pages;
+  a.v_pages = kv.v_pages;
+  a.k_scales = kv.k_scales;
+  a.v_scales = kv.v_scales;
+  a.tok_start = tok_start;
+  a.block_table = block_table;
+  a.seqlens = seqlens;
+  a.geo = kv_geom(kv, pd);
+  a.kv_type = kv.kv_type;
+  a.B = B;
+  a.T = n_tokens;
+  a.D = kv.D;
+  a.cap = pd.max_pages_per_req * pd.page_size;
+  a.k_out = reinterpret_cast<__nv_bfloat16*>(k_out);
+  a.v_out = reinterpret_cast<__nv_bfloat16*>(v_out);
+  return launch_k(sd::kv_load_kernel, dim3(sd::ceil_div(n_tokens, sd::kKvThreads / 32)), dim3(sd::kKvThreads), 0,
+                  static_cast<cudaStream_t>(stream), a);
+}
+
+size_t sd_kv_attn_workspace_size(int32_t B, int32_t G, int32_t H, int32_t D) {
+  if (B < 0 || G <= 0 || H <= 0 || D <= 0 || H % G != 0) return 0;
+  return kv_attn_plan(B, G, H, D).total;
+}
+
+sd_status sd_kv_attn(const uint16_t* q, sd_kv_cache kv, const int32_t* block_table, const int32_t* seqlens,
+                     const int32_t* indices, int32_t n_list, int32_t index_block, sd_paged_desc pd, int32_t B,
+                     int32_t H, float scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  t_launches = 0;
+  const sd_status s = check_kv_attn_args(q, kv, block_table, seqlens, pd, B, H, scale, out);
+  if (s != SD_OK) return s;
+  if (indices == nullptr) n_list = index_block = 1;
+  if (n_list <= 0 || index_block <= 0) return SD_ERR_INVALID_ARG;
+  if ((long long)n_list * index_block >= (1ll << 30)) return SD_ERR_UNSUPPORTED;
+  if (!ws_ok(workspace, workspace_bytes, kv_attn_plan(B, pd.kv_heads, H, kv.D).total)) return SD_ERR_WORKSPACE;
+  if (B == 0) return SD_OK;
+  return launch_kv_attn(q, kv, block_table, seqlens, indices, n_list, index_block, pd, B, H, scale,
+                        pd.max_pages_per_req * pd.page_size, out, lse, workspace, static_cast<cudaStream_t>(stream));
+}
+
+size_t sd_block_topk_workspace_size(int32_t B, int32_t G, int32_t max_seqlen, int32_t block_tokens) {
+  if (B < 0 || G <= 0 || max_seqlen < 0 || block_tokens <= 0) return 0;
+  const int max_blocks = static_cast<int>((max_seqlen + (long long)block_tokens - 1) / block_tokens);
+  return block_keys_bytes(B, G, max_blocks) + align_up(sizeof(int32_t) * (size_t)std::max(B, 1));
+}
+
+sd_status sd_block_topk(const uint16_t* q, sd_kv_cache kv, const int32_t* block_table, const int32_t* seqlens,
+                        sd_paged_desc pd, int32_t B, int32_t H, int32_t max_seqlen, int32_t n_select, int32_t n_first,
+                        int32_t n_last, int32_t* indices, void* workspace, size_t workspace_bytes, void* stream) {
+  t_launches = 0;
+  const sd_status s =
+      check_block_topk_args(q, kv, block_table, seqlens, pd, B, H, max_seqlen, n_select, n_first, n_last, indices);
+  if (s != SD_OK) return s;
+  if (!ws_ok(workspace, workspace_bytes, sd_block_topk_workspace_size(B, pd.kv_heads, max_seqlen, kv.block_tokens)))
+    return SD_ERR_WORKSPACE;
+  if (B == 0) return SD_OK;
+  return launch_block_topk(q, kv, block_table, seqlens, pd, B, H, max_seqlen, n_select, n_first, n_last, indices,
+                           workspace, static_cast<cudaStream_t>(stream));
+}
+
+size_t sd_kv_block_step_workspace_size(int32_t B, int32_t G, int32_t H, int32_t D, int32_t max_seqlen,
+                                       int32_t block_tokens) {
+  const size_t sel = sd_block_topk_workspace_size(B, G, max_seqlen, block_tokens);
+  const size_t att = sd_kv_attn_workspace_size(B, G, H, D);
+  return sel && att ? sel + att : 0;
+}
+
+sd_status sd_kv_block_step(const uint16_t* q, sd_kv_cache kv, const int32_t* block_table, const int32_t* seqlens,
+                           sd_paged_desc pd, int32_t B, int32_t H, int32_t max_seqlen, int32_t n_select,
+                           int32_t n_first, int32_t n_last, float scale, int32_t* indices, uint16_t* out, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  t_launches = 0;
+  sd_status s =
+      check_block_topk_args(q, kv, block_table, seqlens, pd, B, H, max_seqlen, n_select, n_first, n_last, indices);
+  if (s != SD_OK) return s;
+  s = check_kv_attn_args(q, kv, block_table, seqlens, pd, B, H, scale, out);
+  if (s != SD_OK) return s;
+  if (!ws_ok(workspace, workspace_bytes,
+             sd_kv_block_step_workspace_size(B, pd.kv_heads, H, kv.D, max_seqlen, kv.block_tokens)))
+    return SD_ERR_WORKSPACE;
+  if (B == 0) return SD_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  s = launch_block_topk(q, kv, block_table, seqlens, pd, B, H, max_seqlen, n_select, n_first, n_last, indices,
+                        workspace, st);
+  if (s != SD_OK) return s;
+  char* att = static_cast<char*>(workspace) + sd_block_topk_workspace_size(B, pd.kv_heads, max_seqlen, kv.block_tokens);
+  return launch_kv_attn(q, kv, block_table, seqlens, indices, n_select, kv.block_tokens, pd, B, H, scale,
+                        std::min(max_seqlen, pd.max_pages_per_req * pd.page_size), out, lse, att, st);
+}
+
+}  // extern "C"

@@ -2,6 +2,8 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -137,6 +139,21 @@ __device__ __forceinline__ void mma_bf16_16816(float* d, const uint32_t* a, uint
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// n / d for 0 <= n < 2^31 by one widening multiply and a shift: with
+// l = ceil(log2 d) and m = floor(2^(31 + l) / d) + 1, m * d - 2^(31 + l) lies
+// in (0, 2^l], so n * m / 2^(31 + l) exceeds n / d by less than 1 / d.
+struct FastDiv {
+  uint32_t d, m, s;
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * m) >> s);
+  }
+};
+inline FastDiv make_fast_div(int d) {
+  uint32_t l = 0;
+  while ((1u << l) < static_cast<uint32_t>(d)) ++l;
+  return FastDiv{static_cast<uint32_t>(d), static_cast<uint32_t>((1ull << (31 + l)) / static_cast<uint32_t>(d) + 1), 31 + l};
 }
 
 __host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
