@@ -5,9 +5,10 @@
 //   y = x * rsqrt(mean(x^2) + eps) * w          (skipped where w is null)
 //   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[i],
 //   over the pairs (i, i + R/2), or (2i, 2i + 1), of the first R dims.
-// The angle is taken in turns in fp64 and reduced to [-1/2, 1/2] before it is
-// rounded to fp32 (a far position times a frequency keeps only a few bits of
-// its fraction in fp32). q is rounded once to bf16. K and V go into a bf16,
+// The angle is taken in turns, with the frequency as a 64-bit fixed-point
+// fraction of a turn: position times frequency modulo one turn is an integer
+// product modulo 2^64, exact to 2^-34 turns at any 32-bit position, where a
+// far position times a frequency in fp32 keeps only a few bits of its fraction. q is rounded once to bf16. K and V go into a bf16,
 // int8 or e4m3 pool. An 8-bit pool is cut into blocks of `bs` consecutive
 // slots (a page holds whole blocks); a block and KV head have one scale for K
 // and one for V:
@@ -20,12 +21,14 @@
 // The block's bounds (smallest and largest bf16(y) of K for every dim) are
 // what the block selection reads.
 //
-// Work split. K and V: one CTA per (touched block, KV head), since the scale
-// needs the whole block's rows before any of them is coded; the rows stay in
-// registers in between. q: one group of D / 8 lanes per (token, group of
-// heads); the token's angles are computed once per group and used for its
-// heads. Bound by HBM for prompts and by launch and load latency for a
-// decode step.
+// Work split, one launch. K and V: the scale needs all of a block's new rows
+// before any is coded. A prompt gets one CTA per (touched block, KV head),
+// which keeps the rotated rows in shared memory in between; a decode step one
+// warp per (token, KV head), K in one part of its lanes and V in the other,
+// and units of several rows fall back to the whole CTA. q: one group of D / 8 lanes per (token,
+// group of heads); the token's angles are computed once per group and used
+// for its heads. Bound by HBM for prompts and by launch and load latency
+// for a decode step.
 #pragma once
 
 #include <float.h>
@@ -72,6 +75,9 @@ __device__ __forceinline__ float2 bf2(uint32_t w) {
 // group together: one load a lane and step. l is the lane in its group.
 template <int LANES>
 __device__ __forceinline__ int find_request(const int32_t* tok_start, int B, int r, int l) {
+  // in a decode step row r is request r's only one: one load settles that
+  const int guess = min(r, B - 1);
+  if (__all_sync(0xffffffffu, tok_start[guess] <= r && r < tok_start[guess + 1])) return guess;
   const int base = (threadIdx.x & 31) & ~(LANES - 1);
   int lo = 0;
   for (int span = B; span > 1;) {
@@ -118,23 +124,27 @@ __device__ __forceinline__ void norm_row(float* e, const float* w, float eps) {
 template <int D, bool FULL>
 struct Rotation {
   static constexpr int N = FULL ? 4 : 8;
-  double f[N];  // turns per position (0: not rotated)
+  unsigned long long f[N];  // turns per position, modulo one turn, in units of 2^-64 (0: not rotated)
   float c[N], s[N];
 
   __device__ __forceinline__ void init(const float* inv_freq, int R, bool interleaved, int l) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int d = (j < 4 ? 0 : D / 2 - 4) + 4 * l + j;
-      int i = interleaved ? d >> 1 : (d < R / 2 ? d : d - R / 2);
-      f[j] = d < R || FULL ? static_cast<double>(inv_freq[i]) * 0.15915494309189535 : 0.0;
+      const int i = interleaved ? d >> 1 : (d < R / 2 ? d : d - R / 2);
+      f[j] = 0;
+      if (d < R) {
+        const double t = static_cast<double>(inv_freq[i]) * 0.15915494309189535;  // 1 / (2 pi)
+        const double u = (t - floor(t)) * 18446744073709551616.0;                 // [0, 2^64]
+        f[j] = u < 18446744073709551616.0 ? __double2ull_rn(u) : 0ull;
+      }
     }
   }
   __device__ __forceinline__ void at(int pos) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      double t = static_cast<double>(pos) * f[j];
-      t -= rint(t);
-      sincospif(2.f * static_cast<float>(t), &s[j], &c[j]);
+      const unsigned long long t = static_cast<unsigned long long>(static_cast<long long>(pos)) * f[j];
+      sincospif(static_cast<float>(static_cast<int>(t >> 32)) * 4.656612873077393e-10f, &s[j], &c[j]);  // 2^-31
     }
   }
   __device__ __forceinline__ void apply(float* e, int R, bool interleaved, int l) const {
@@ -215,10 +225,13 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= FLT_MAX ? a : 0.f;
 }
 
-// Codes of rows [0, n) at row pitch G * D re-scaled by ratio < 1.
-__device__ __forceinline__ void recode_rows(uint8_t* first, long long pitch, int n, int D, float ratio, int kv_type) {
+// Codes of rows [0, n), `pitch` bytes apart, scaled by ratio < 1, by `threads`
+// threads of which this is number `i0`.
+__device__ __forceinline__ void recode_rows(uint8_t* first, long long pitch, int n, int D, float ratio, int kv_type, int i0,
+                                            int threads) {
   const int per_row = D / 16;
-  for (int i = threadIdx.x; i < n * per_row; i += kKvThreads) {
+#pragma unroll 2
+  for (int i = i0; i < n * per_row; i += threads) {
     uint4* at = reinterpret_cast<uint4*>(first + (i / per_row) * pitch + (i % per_row) * 16);
     uint4 w = *at;
     uint32_t* u = reinterpret_cast<uint32_t*>(&w);
@@ -261,8 +274,8 @@ template <int D, bool FULL>
 __device__ void store_queries(const KvStoreArgs& a) {
   constexpr int LANES = D / 8, GROUPS = kKvThreads / LANES;
   const int l = threadIdx.x % LANES;
-  const long long item = (long long)(blockIdx.x - a.kv_ctas) * GROUPS + threadIdx.x / LANES;
-  const int token = static_cast<int>(item / a.head_groups), hg = static_cast<int>(item % a.head_groups);
+  const int item = (blockIdx.x - a.kv_ctas) * GROUPS + threadIdx.x / LANES;
+  const int token = item / a.head_groups, hg = item - token * a.head_groups;
   const bool in = token < a.T;
   const int b = find_request<LANES>(a.tok_start, a.B, in ? token : 0, l);
   const bool ok = in && token >= a.tok_start[0] && token < a.tok_start[a.B];
@@ -304,184 +317,165 @@ __device__ void store_queries(const KvStoreArgs& a) {
   }
 }
 
-template <int D, bool FULL>
-__device__ void store_block(const KvStoreArgs& a) {
-  constexpr int LANES = D / 8, RPP = kKvThreads / LANES, PASSES = kKvMaxBlock / RPP;
-  __shared__ int s_unit[2];
-  __shared__ int s_scan[kKvThreads / 32];
-  __shared__ float s_amax[2][kKvThreads / 32];
-  __shared__ float s_bounds[2][kKvThreads / 32][D];
-  const KvGeom& geo = a.geo;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = tid % LANES;
-  const int unit = blockIdx.x / geo.G, g = blockIdx.x % geo.G, bs = geo.bs;
+// One touched block of a request, under one KV head.
+struct KvUnit {
+  int b, c;        // request, block
+  int row0, nr;    // its first new row and how many
+  int lo;          // position of the first
+  long long blk;   // index of its scales and bounds
+  long long base;  // its first pool row
+  bool ok;
+};
 
-  // ---- which request and block this unit is ----
-  int b, c, r0, p0, p1;  // block c of request b; its first new row and its new positions [p0, p1)
-  if (a.by_row) {
-    b = find_request<32>(a.tok_start, a.B, unit, lane);
-    if (unit < a.tok_start[0] || unit >= a.tok_start[a.B]) return;
-    const int p = row_position(a, b, unit, &r0, &p0, &p1);
-    if (p < 0) return;
-    c = geo.bs_div.div(p);
-    if (p != c * bs && unit != r0 && p != 0) return;  // the block belongs to an earlier row
-  } else {
-    if (tid == 0) s_unit[0] = -1;
-    int before = 0;
-    for (int base = 0; base < a.B; base += kKvThreads) {
-      const int i = base + tid;
-      int n = 0;
-      if (i < a.B) {
-        int fr, q0, q1;
-        row_position(a, i, 0, &fr, &q0, &q1);
-        q0 = max(q0, 0);
-        n = q1 > q0 ? geo.bs_div.div(q1 - 1) - geo.bs_div.div(q0) + 1 : 0;
-      }
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      if (lane == 31) s_scan[warp] = incl;
-      __syncthreads();
-      int skip = before, all = 0;
-      for (int w = 0; w < kKvThreads / 32; ++w) {
-        skip += w < warp ? s_scan[w] : 0;
-        all += s_scan[w];
-      }
-      const int e = skip + incl;
-      if (unit < e && unit >= e - n) s_unit[0] = i, s_unit[1] = unit - (e - n);
-      before += all;
-      __syncthreads();
-      if (s_unit[0] >= 0) break;
-    }
-    if (s_unit[0] < 0) return;
-    b = s_unit[0];
-    row_position(a, b, 0, &r0, &p0, &p1);
-    c = geo.bs_div.div(max(p0, 0)) + s_unit[1];
+// Block c of request b with new positions [p0, p1), whose first is row r0. `raise`: whether this
+// thread reports bad data.
+__device__ __forceinline__ KvUnit make_unit(const KvStoreArgs& a, int b, int c, int r0, int p0, int p1, int g, bool raise) {
+  const KvGeom& geo = a.geo;
+  KvUnit u;
+  u.b = b, u.c = c, u.ok = false;
+  u.lo = max(max(p0, 0), c * geo.bs);
+  u.row0 = r0 + (u.lo - p0);
+  u.nr = min(min(p1, c * geo.bs + geo.bs) - u.lo, a.T - u.row0);
+  u.blk = u.base = 0;
+  if (u.row0 < 0 || u.nr <= 0) {
+    if (raise) raise_error(SD_DEVERR_INDEX);
+    return u;
   }
-  const int lo = max(max(p0, 0), c * bs), hi = min(p1, c * bs + bs);
-  const int row0 = r0 + (lo - p0);
-  const int nr = min(hi - lo, a.T - row0);
-  if (row0 < 0 || nr <= 0) {
-    if (tid == 0) raise_error(SD_DEVERR_INDEX);
-    return;
-  }
-  const int pi = geo.page_div.div(c * bs);
+  const int pi = geo.page_div.div(c * geo.bs);
   const int page = a.block_table[(size_t)b * geo.max_pages + pi];
   if (page < 0 || page >= geo.num_pages) {
-    if (tid == 0) raise_error(SD_DEVERR_PAGE);
-    return;
+    if (raise) raise_error(SD_DEVERR_PAGE);
+    return u;
   }
-  const int slot0 = c * bs - pi * geo.page_size;                 // the block's first slot
-  const long long blk = ((long long)page * geo.blocks_per_page + geo.bs_div.div(slot0)) * geo.G + g;
-  const long long row_base = (long long)page * geo.page_size + slot0;  // its pool row
-  const bool earlier = lo > c * bs;
+  const int slot0 = c * geo.bs - pi * geo.page_size;
+  u.blk = ((long long)page * geo.blocks_per_page + geo.bs_div.div(slot0)) * geo.G + g;
+  u.base = (long long)page * geo.page_size + slot0;
+  u.ok = true;
+  return u;
+}
 
-  // ---- load the new rows, norm and rotate K, find both maxima ----
-  uint2 vx[PASSES], vy[PASSES];
-  float e[PASSES][8];
-#pragma unroll
-  for (int ps = 0; ps < PASSES; ++ps) {
-    const int i = ps * RPP + tid / LANES;
-    uint2 x = make_uint2(0u, 0u), y = x;
-    vx[ps] = vy[ps] = x;
-    if (ps * RPP < nr && i < nr) {
-      const __nv_bfloat16* ks = a.k + (row0 + i) * a.k_stride + (long long)g * D + 4 * l;
-      const __nv_bfloat16* vs = a.v + (row0 + i) * a.v_stride + (long long)g * D + 4 * l;
-      x = *reinterpret_cast<const uint2*>(ks);
-      y = *reinterpret_cast<const uint2*>(ks + D / 2);
-      vx[ps] = *reinterpret_cast<const uint2*>(vs);
-      vy[ps] = *reinterpret_cast<const uint2*>(vs + D / 2);
-    }
-    unpack_row<D>(x, y, e[ps]);
-  }
+template <int D>
+struct KvBlockSmem {
+  float amax[2][kKvThreads / 32];
+  float bounds[2][kKvThreads / 32][D];
+  int scan[kKvThreads / 32];
+  int unit[2];
+  KvUnit units[kKvThreads / 32];
+};
+
+// A unit of any number of rows, by the whole CTA. `rows` holds block_tokens x
+// D floats of the rotated K.
+template <int D, bool FULL>
+__device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBlockSmem<D>& sm, float* rows) {
+  constexpr int LANES = D / 8, RPP = kKvThreads / LANES;
+  const KvGeom& geo = a.geo;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = tid % LANES, bs = geo.bs;
+  const bool earlier = u.lo > u.c * bs, quant = a.kv_type != SD_KV_BF16;
+  const float old_k = earlier && quant ? a.k_scales[u.blk] : 0.f, old_v = earlier && quant ? a.v_scales[u.blk] : 0.f;
   Rotation<D, FULL> rot;
   rot.init(a.inv_freq, a.R, a.interleaved, l);
   float w[8];
   if (a.kw != nullptr) load_weight<D>(a.kw, l, w);
+  const __nv_bfloat16* ks = a.k + u.row0 * a.k_stride + (long long)g * D + 4 * l;
+  const __nv_bfloat16* vs = a.v + u.row0 * a.v_stride + (long long)g * D + 4 * l;
   float mk = 0.f, mv = 0.f, bmin[8], bmax[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) bmin[j] = INFINITY, bmax[j] = -INFINITY;
-#pragma unroll
-  for (int ps = 0; ps < PASSES; ++ps) {
-    if (ps * RPP >= nr) break;
-    const int i = ps * RPP + tid / LANES;
-    if (a.kw != nullptr) norm_row<D>(e[ps], w, a.eps);
-    if (a.R > 0) {
-      rot.at(i < nr && a.positions != nullptr ? a.positions[row0 + i] : lo + i);
-      rot.apply(e[ps], a.R, a.interleaved, l);
+#pragma unroll 1
+  for (int i0 = 0; i0 < u.nr; i0 += RPP) {
+    const int i = i0 + tid / LANES;
+    const bool in = i < u.nr;
+    uint2 x = make_uint2(0u, 0u), y = x, vx = x, vy = x;
+    if (in) {
+      x = *reinterpret_cast<const uint2*>(ks + i * a.k_stride);
+      y = *reinterpret_cast<const uint2*>(ks + i * a.k_stride + D / 2);
+      vx = *reinterpret_cast<const uint2*>(vs + i * a.v_stride);
+      vy = *reinterpret_cast<const uint2*>(vs + i * a.v_stride + D / 2);
     }
-    if (i < nr) {
+    float e[8];
+    unpack_row<D>(x, y, e);
+    if (a.kw != nullptr) norm_row<D>(e, w, a.eps);
+    if (a.R > 0) {
+      rot.at(in && a.positions != nullptr ? a.positions[u.row0 + i] : u.lo + i);
+      rot.apply(e, a.R, a.interleaved, l);
+    }
+    if (in) {
       float v[8];
-      unpack_row<D>(vx[ps], vy[ps], v);
+      unpack_row<D>(vx, vy, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        mk = fmaxf(mk, finite_abs(e[ps][j]));
+        mk = fmaxf(mk, finite_abs(e[j]));
         mv = fmaxf(mv, finite_abs(v[j]));
-        const float kb = __bfloat162float(__float2bfloat16_rn(e[ps][j]));
+        const float kb = __bfloat162float(__float2bfloat16_rn(e[j]));
         bmin[j] = fminf(bmin[j], kb);
         bmax[j] = fmaxf(bmax[j], kb);
       }
+      if (quant) {
+        *reinterpret_cast<float4*>(rows + i * D + 4 * l) = make_float4(e[0], e[1], e[2], e[3]);
+        *reinterpret_cast<float4*>(rows + i * D + D / 2 + 4 * l) = make_float4(e[4], e[5], e[6], e[7]);
+      } else {
+        const long long row = (u.base + (u.lo - u.c * bs) + i) * geo.G + g;
+        store_row<D>(a.k_pages, row, l, e, 1.f, SD_KV_BF16);
+        store_row<D>(a.v_pages, row, l, v, 1.f, SD_KV_BF16);
+      }
     }
   }
-
-  const bool quant = a.kv_type != SD_KV_BF16;
-  float sk = 1.f, sv = 1.f;
   if (quant) {
-    const float ok = earlier ? a.k_scales[blk] : 0.f, ov = earlier ? a.v_scales[blk] : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
       mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
     }
-    if (lane == 0) s_amax[0][warp] = mk, s_amax[1][warp] = mv;
-    __syncthreads();  // also: every thread has read the old scales
-    for (int i = 0; i < kKvThreads / 32; ++i) mk = fmaxf(mk, s_amax[0][i]), mv = fmaxf(mv, s_amax[1][i]);
+    if (lane == 0) sm.amax[0][warp] = mk, sm.amax[1][warp] = mv;
+  }
+  if (a.bounds != nullptr) {
+#pragma unroll
+    for (int o = LANES; o < 32; o <<= 1) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        bmin[j] = fminf(bmin[j], __shfl_xor_sync(0xffffffffu, bmin[j], o));
+        bmax[j] = fmaxf(bmax[j], __shfl_xor_sync(0xffffffffu, bmax[j], o));
+      }
+    }
+    if (lane < LANES) {
+      *reinterpret_cast<float4*>(&sm.bounds[0][warp][4 * l]) = make_float4(bmin[0], bmin[1], bmin[2], bmin[3]);
+      *reinterpret_cast<float4*>(&sm.bounds[0][warp][D / 2 + 4 * l]) = make_float4(bmin[4], bmin[5], bmin[6], bmin[7]);
+      *reinterpret_cast<float4*>(&sm.bounds[1][warp][4 * l]) = make_float4(bmax[0], bmax[1], bmax[2], bmax[3]);
+      *reinterpret_cast<float4*>(&sm.bounds[1][warp][D / 2 + 4 * l]) = make_float4(bmax[4], bmax[5], bmax[6], bmax[7]);
+    }
+  }
+  __syncthreads();  // also: every thread has read the old scales
+  if (quant) {
+    for (int i = 0; i < kKvThreads / 32; ++i) mk = fmaxf(mk, sm.amax[0][i]), mv = fmaxf(mv, sm.amax[1][i]);
     const float qmax = a.kv_type == SD_KV_INT8 ? 127.f : 448.f;
-    sk = fmaxf(fmaxf(mk / qmax, kKvMinScale), ok);
-    sv = fmaxf(fmaxf(mv / qmax, kKvMinScale), ov);
+    const float sk = fmaxf(fmaxf(mk / qmax, kKvMinScale), old_k), sv = fmaxf(fmaxf(mv / qmax, kKvMinScale), old_v);
     if (earlier) {
-      const long long at = (row_base * geo.G + g) * D, pitch = (long long)geo.G * D;
-      if (sk > ok) recode_rows(static_cast<uint8_t*>(a.k_pages) + at, pitch, lo - c * bs, D, ok / sk, a.kv_type);
-      if (sv > ov) recode_rows(static_cast<uint8_t*>(a.v_pages) + at, pitch, lo - c * bs, D, ov / sv, a.kv_type);
+      const long long at = (u.base * geo.G + g) * D, pitch = (long long)geo.G * D;
+      const int n = u.lo - u.c * bs;
+      if (sk > old_k) recode_rows(static_cast<uint8_t*>(a.k_pages) + at, pitch, n, D, old_k / sk, a.kv_type, tid, kKvThreads);
+      if (sv > old_v) recode_rows(static_cast<uint8_t*>(a.v_pages) + at, pitch, n, D, old_v / sv, a.kv_type, tid, kKvThreads);
     }
-    if (tid == 0) a.k_scales[blk] = sk, a.v_scales[blk] = sv;
-  }
-  const float ik = 1.f / sk, iv = 1.f / sv;
-#pragma unroll
-  for (int ps = 0; ps < PASSES; ++ps) {
-    const int i = ps * RPP + tid / LANES;
-    if (i >= nr) break;
-    const long long row = (row_base + (lo - c * bs) + i) * geo.G + g;
-    store_row<D>(a.k_pages, row, l, e[ps], ik, a.kv_type);
-    float v[8];
-    unpack_row<D>(vx[ps], vy[ps], v);
-    store_row<D>(a.v_pages, row, l, v, iv, a.kv_type);
-  }
-  if (a.bounds == nullptr) return;
-#pragma unroll
-  for (int o = LANES; o < 32; o <<= 1) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      bmin[j] = fminf(bmin[j], __shfl_xor_sync(0xffffffffu, bmin[j], o));
-      bmax[j] = fmaxf(bmax[j], __shfl_xor_sync(0xffffffffu, bmax[j], o));
+    if (tid == 0) a.k_scales[u.blk] = sk, a.v_scales[u.blk] = sv;
+    const float ik = 1.f / sk, iv = 1.f / sv;
+#pragma unroll 2
+    for (int i = tid / LANES; i < u.nr; i += RPP) {
+      const uint2 vx = *reinterpret_cast<const uint2*>(vs + i * a.v_stride);  // read before, still in L2
+      const uint2 vy = *reinterpret_cast<const uint2*>(vs + i * a.v_stride + D / 2);
+      const float4 x = *reinterpret_cast<const float4*>(rows + i * D + 4 * l);
+      const float4 y = *reinterpret_cast<const float4*>(rows + i * D + D / 2 + 4 * l);
+      const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      const long long row = (u.base + (u.lo - u.c * bs) + i) * geo.G + g;
+      store_row<D>(a.k_pages, row, l, e, ik, a.kv_type);
+      float v[8];
+      unpack_row<D>(vx, vy, v);
+      store_row<D>(a.v_pages, row, l, v, iv, a.kv_type);
     }
   }
-  if (lane < LANES) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int d = (j < 4 ? 0 : D / 2 - 4) + 4 * l + j;
-      s_bounds[0][warp][d] = bmin[j];
-      s_bounds[1][warp][d] = bmax[j];
-    }
-  }
-  __syncthreads();
-  if (tid < 2 * D) {
+  if (a.bounds != nullptr && tid < 2 * D) {
     const int which = tid / D, d = tid % D;
-    __nv_bfloat16* at = a.bounds + (blk * 2 + which) * D + d;
-    float x = s_bounds[which][0][d];
-    for (int i = 1; i < kKvThreads / 32; ++i) x = which ? fmaxf(x, s_bounds[1][i][d]) : fminf(x, s_bounds[0][i][d]);
+    __nv_bfloat16* at = a.bounds + (u.blk * 2 + which) * D + d;
+    float x = sm.bounds[which][0][d];
+    for (int i = 1; i < kKvThreads / 32; ++i) x = which ? fmaxf(x, sm.bounds[1][i][d]) : fminf(x, sm.bounds[0][i][d]);
     if (earlier) {
       const float old = __bfloat162float(*at);
       x = which ? fmaxf(x, old) : fminf(x, old);
@@ -490,12 +484,174 @@ __device__ void store_block(const KvStoreArgs& a) {
   }
 }
 
+// A unit of one row, by one warp: lanes [0, D/8) hold K, [D/8, D/4) hold V.
 template <int D, bool FULL>
-__global__ void __launch_bounds__(kKvThreads) kv_store_kernel(const __grid_constant__ KvStoreArgs a) {
+__device__ void store_unit_warp(const KvStoreArgs& a, const KvUnit& u, int g, uint2 x, uint2 y) {
+  constexpr int LANES = D / 8;
+  const KvGeom& geo = a.geo;
+  const int lane = threadIdx.x & 31, l = lane % LANES, bs = geo.bs;
+  const bool is_v = lane / LANES == 1, live = lane < 2 * LANES;
+  const bool earlier = u.lo > u.c * bs, quant = a.kv_type != SD_KV_BF16;
+  float* scales = is_v ? a.v_scales : a.k_scales;
+  void* pages = is_v ? a.v_pages : a.k_pages;
+  const float old = earlier && quant ? scales[u.blk] : 0.f;
+  uint2 ob[2][2];  // the block's bounds so far
+  __nv_bfloat16* at = a.bounds + u.blk * 2 * D + 4 * l;
+  if (a.bounds != nullptr && earlier && lane < LANES) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ob[i][0] = *reinterpret_cast<const uint2*>(at + i * D);
+      ob[i][1] = *reinterpret_cast<const uint2*>(at + i * D + D / 2);
+    }
+  }
+  float e[8], v[8];
+  unpack_row<D>(x, y, e);
+  unpack_row<D>(x, y, v);
+  if (a.kw != nullptr) {
+    float w[8];
+    load_weight<D>(a.kw, l, w);
+    norm_row<D>(e, w, a.eps);
+  }
+  if (a.R > 0) {
+    Rotation<D, FULL> rot;
+    rot.init(a.inv_freq, a.R, a.interleaved, l);
+    rot.at(a.positions != nullptr ? a.positions[u.row0] : u.lo);
+    rot.apply(e, a.R, a.interleaved, l);
+  }
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    e[j] = is_v ? v[j] : e[j];
+    m = fmaxf(m, finite_abs(e[j]));
+  }
+  float inv = 1.f;
+  if (quant) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float qmax = a.kv_type == SD_KV_INT8 ? 127.f : 448.f;
+    const float s = fmaxf(fmaxf(m / qmax, kKvMinScale), old);
+    inv = 1.f / s;
+    if (earlier) {
+      const float sk = __shfl_sync(0xffffffffu, s, 0), sv = __shfl_sync(0xffffffffu, s, LANES);
+      const float ok = __shfl_sync(0xffffffffu, old, 0), ov = __shfl_sync(0xffffffffu, old, LANES);
+      const long long first = (u.base * geo.G + g) * D, pitch = (long long)geo.G * D;
+      const int n = u.lo - u.c * bs;
+      if (sk > ok) recode_rows(static_cast<uint8_t*>(a.k_pages) + first, pitch, n, D, ok / sk, a.kv_type, lane, 32);
+      if (sv > ov) recode_rows(static_cast<uint8_t*>(a.v_pages) + first, pitch, n, D, ov / sv, a.kv_type, lane, 32);
+    }
+    if (live && l == 0) scales[u.blk] = s;
+  }
+  if (live) store_row<D>(pages, (u.base + (u.lo - u.c * bs)) * geo.G + g, l, e, inv, a.kv_type);
+  if (a.bounds == nullptr || lane >= LANES) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float z[8], o[8];
+    unpack_row<D>(ob[i][0], ob[i][1], o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      z[j] = __bfloat162float(__float2bfloat16_rn(e[j]));
+      if (z[j] != z[j]) z[j] = i ? -INFINITY : INFINITY;  // a NaN key bounds nothing
+      if (earlier) z[j] = i ? fmaxf(z[j], o[j]) : fminf(z[j], o[j]);
+    }
+    *reinterpret_cast<uint2*>(at + i * D) = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+    *reinterpret_cast<uint2*>(at + i * D + D / 2) = make_uint2(pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
+  }
+}
+
+// Units by row: warp w of the CTA takes (row, KV head) pair w, if the row is
+// the first new one of its block.
+template <int D, bool FULL>
+__device__ void store_by_row(const KvStoreArgs& a, KvBlockSmem<D>& sm, float* rows) {
+  constexpr int LANES = D / 8, kWarps = kKvThreads / 32;
+  const KvGeom& geo = a.geo;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES;
+  const int item = blockIdx.x * kWarps + warp, row = item / geo.G, g = item - row * geo.G;
+  KvUnit u;
+  u.ok = false, u.nr = 0;
+  uint2 x = make_uint2(0u, 0u), y = x;
+  if (row < a.T) {
+    const __nv_bfloat16* src = lane / LANES == 1 ? a.v + row * a.v_stride : a.k + row * a.k_stride;
+    if (lane < 2 * LANES) {  // needed whether or not the row is the first of its block
+      x = *reinterpret_cast<const uint2*>(src + (long long)g * D + 4 * l);
+      y = *reinterpret_cast<const uint2*>(src + (long long)g * D + D / 2 + 4 * l);
+    }
+    const int b = find_request<32>(a.tok_start, a.B, row, lane);
+    if (row >= a.tok_start[0] && row < a.tok_start[a.B]) {
+      int r0, p0, p1;
+      const int p = row_position(a, b, row, &r0, &p0, &p1);
+      if (p >= 0 && p < p1) {
+        const int c = geo.bs_div.div(p);
+        if (p == c * geo.bs || row == r0) u = make_unit(a, b, c, r0, p0, p1, g, lane == 0);
+      }
+    }
+  }
+  if (u.ok && u.nr == 1) store_unit_warp<D, FULL>(a, u, g, x, y);
+  // units of several rows (several tokens of a request among single ones)
+  const bool many = u.ok && u.nr > 1;
+  if (lane == 0) sm.units[warp] = u;
+  if (!__syncthreads_or(many)) return;
+  for (int w = 0; w < kWarps; ++w) {
+    const KvUnit v = sm.units[w];
+    if (!v.ok || v.nr <= 1) continue;
+    store_unit_cta<D, FULL>(a, v, (blockIdx.x * kWarps + w) % geo.G, sm, rows);
+    __syncthreads();  // its shared memory is free again
+  }
+}
+
+// Units by touched block: unit u of the list over all requests, one CTA per
+// KV head.
+template <int D, bool FULL>
+__device__ void store_by_block(const KvStoreArgs& a, KvBlockSmem<D>& sm, float* rows) {
+  const KvGeom& geo = a.geo;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int unit = blockIdx.x / geo.G, g = blockIdx.x % geo.G;
+  int r0, p0, p1;
+  if (tid == 0) sm.unit[0] = -1;
+  int before = 0;
+  for (int base = 0; base < a.B; base += kKvThreads) {
+    const int i = base + tid;
+    int n = 0;
+    if (i < a.B) {
+      row_position(a, i, 0, &r0, &p0, &p1);
+      p0 = max(p0, 0);
+      n = p1 > p0 ? geo.bs_div.div(p1 - 1) - geo.bs_div.div(p0) + 1 : 0;
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) sm.scan[warp] = incl;
+    __syncthreads();
+    int skip = before, all = 0;
+    for (int w = 0; w < kKvThreads / 32; ++w) {
+      skip += w < warp ? sm.scan[w] : 0;
+      all += sm.scan[w];
+    }
+    const int e = skip + incl;
+    if (unit < e && unit >= e - n) sm.unit[0] = i, sm.unit[1] = unit - (e - n);
+    before += all;
+    __syncthreads();
+    if (sm.unit[0] >= 0) break;
+  }
+  if (sm.unit[0] < 0) return;
+  const int b = sm.unit[0];
+  row_position(a, b, 0, &r0, &p0, &p1);
+  const KvUnit u = make_unit(a, b, geo.bs_div.div(max(p0, 0)) + sm.unit[1], r0, p0, p1, g, tid == 0);
+  if (u.ok) store_unit_cta<D, FULL>(a, u, g, sm, rows);
+}
+
+template <int D, bool FULL>
+__global__ void __launch_bounds__(kKvThreads, 3) kv_store_kernel(const __grid_constant__ KvStoreArgs a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ KvBlockSmem<D> sm;
   pdl_wait();  // inputs come from earlier work in the stream
   pdl_trigger();
-  if (blockIdx.x < a.kv_ctas) store_block<D, FULL>(a);
-  else store_queries<D, FULL>(a);
+  float* rows = reinterpret_cast<float*>(smem_raw);
+  if (blockIdx.x >= a.kv_ctas) store_queries<D, FULL>(a);
+  else if (a.by_row) store_by_row<D, FULL>(a, sm, rows);
+  else store_by_block<D, FULL>(a, sm, rows);
 }
 
 // Reads the tokens that a store with the same tok_start and seqlens wrote back

@@ -1200,11 +1200,12 @@ sd_status sd_kv_store(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
   a.R = rot_dim;
   a.interleaved = interleaved != 0;
   a.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
-  // a request touches at most n / block_tokens + 2 blocks; where that does not
-  // beat one unit per row, rows are the units and need no search over requests
+  // A request touches at most n / block_tokens + 2 blocks. Where that does not
+  // beat one unit per row (a decode step), rows are the units, a warp each.
   const long long touched = n_tokens / kv.block_tokens + 2ll * B;
   a.by_row = n_tokens <= touched;
-  const long long kv_ctas = std::min<long long>(n_tokens, touched) * G;
+  const int warps = sd::kKvThreads / 32;
+  const long long kv_ctas = a.by_row ? ((long long)n_tokens * G + warps - 1) / warps : touched * G;
   // heads per lane group: as many as leave two waves of groups
   const int groups = sd::kKvThreads / (kv.D / 8);
   a.heads_per_group = std::max(1, std::min(a.H, 32));
@@ -1213,12 +1214,16 @@ sd_status sd_kv_store(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
     a.heads_per_group = (a.heads_per_group + 1) / 2;
   a.head_groups = sd::ceil_div(a.H, a.heads_per_group);
   const long long q_ctas = ((long long)n_tokens * a.head_groups + groups - 1) / groups;
-  if (kv_ctas + q_ctas >= (1ll << 31)) return SD_ERR_UNSUPPORTED;
+  if (kv_ctas + q_ctas >= (1ll << 31) || (long long)n_tokens * std::max(G, a.head_groups) >= (1ll << 31) - 1024)
+    return SD_ERR_UNSUPPORTED;
   if (B == 0 || n_tokens == 0) return SD_OK;
   a.kv_ctas = static_cast<int>(kv_ctas);
   auto kern = kv.D == 64 ? (full ? sd::kv_store_kernel<64, true> : sd::kv_store_kernel<64, false>)
                          : (full ? sd::kv_store_kernel<128, true> : sd::kv_store_kernel<128, false>);
-  return launch_k(kern, dim3(static_cast<unsigned>(kv_ctas + q_ctas)), dim3(sd::kKvThreads), 0,
+  // the rotated K of a block between its two passes (8-bit pools)
+  const size_t smem = kv.kv_type == SD_KV_BF16 ? 0 : (size_t)kv.block_tokens * kv.D * sizeof(float);
+  if (smem > 32 * 1024 && (s = set_smem_limit(reinterpret_cast<const void*>(kern), smem)) != SD_OK) return s;
+  return launch_k(kern, dim3(static_cast<unsigned>(kv_ctas + q_ctas)), dim3(sd::kKvThreads), smem,
                   static_cast<cudaStream_t>(stream), a);
 }
 
