@@ -6,29 +6,34 @@
 // `index_block` tokens per (request, KV head) (1: the tokens an indexer
 // selects).
 //
-// Mathematics. Codes are exact in fp16, so both products run on fp16 matrix
-// instructions with fp32 sums; q is scaled per head by a power of two so that
-// its largest magnitude lies in [2^14, 2^15), where every bf16 value down to
-// 2^-28 of it is exact in fp16. V's scale joins the exponent: with base-2
-// logits z and u_j = z_j + log2 sv_j, the weights a_j = 2^(u_j - M) <= 2^8
-// multiply the raw codes in fp16 (one rounding, 2^-11) and the sum of
-// 2^(z_j - M) in fp32 divides them at the end. One reference M serves both, and
-// it follows the running maximum of u lazily: only a value more than 8 above
-// it moves it, so the common tile takes no shuffle for the maximum and no
-// rescale.
+// Mathematics. q . k8 runs on the 8-bit matrix instructions with K's codes
+// as they lie in the cache: q is cut into parts of the cache's own type whose
+// weighted sum is q. int8: q * S rounded to a 23-bit integer (S a power of
+// two, so bf16 values down to 2^-14 of the head's largest are exact), three
+// signed base-256 digits, int32 sums. e4m3: the rounding of q * S and the
+// rounding of 16 times what it left, which hold a bf16 value's 8 bits down to 2^-14
+// of the largest; fp32 sums. The decode group's few heads leave columns of the instruction
+// free, which the parts fill. P.V runs on fp16 instructions with fp32 sums:
+// codes are exact in fp16, weights rounded to fp16 (2^-11). V's scale joins the exponent: with
+// base-2 logits z and u_j = z_j + log2 sv_j, the weights a_j = 2^(u_j - M)
+// <= 2^8 multiply V's codes, and the sum of a_j / sv_j = 2^(z_j - M), in fp32
+// from the weights before their rounding, divides them at the end. One
+// reference M serves both, and it follows the running maximum of u lazily: only a value more
+// than 8 above it moves it, so the common tile takes no shuffle for the
+// maximum and no rescale.
 //
-// Layout. Everything is warp-private: a warp owns one KV head (8 * NT query
-// heads of it) and streams its tokens 16 at a time through a ring of cp.async
-// stages in shared memory; warps of a CTA take the heads of the same tokens,
-// so that a CTA's copies cover whole contiguous pool rows. No barrier is needed after the work
-// list is set up. Both products take the cache as the matrix instruction's A operand (S^T = K Q^T
-// and O^T = V^T P^T: M = 16 tokens or dims, N = 8 heads), since a decode
-// group has few query heads: m16n8k16 then wastes half of what heads as M = 16
-// would. The order of the contracted dims is free as long as q and K agree, as is the
-// order of V's dims, so each lane reads 16-byte pieces of rows and unpacks
-// them in registers straight into fragments; no transposing load is needed.
+// Layout. Everything is warp-private: a warp owns up to 16 query heads of one
+// KV head and streams its tokens through a ring of 16-token cp.async stages
+// in shared memory; warps of a CTA take the heads of the same tokens, so that
+// a CTA's copies cover whole contiguous pool rows. There is no barrier
+// anywhere. Both products take the cache as the matrix instruction's A
+// operand (S^T = K Q^T and O^T = V^T P^T: M = 16 tokens or dims, N = 8
+// columns of heads and parts). The order of the contracted dims is free as
+// long as q and K agree, as is the order of V's dims, so each lane reads
+// 16-byte pieces of rows that are fragments already (K) or become some by
+// byte permutes (V); no transposing load is needed.
 //
-// Split. The tokens of all requests form one list of 16-token tiles, cut into
+// Split. The tokens of all requests form one list of 32-token tiles, cut into
 // equal ranges of one resident wave of CTAs; a range that crosses requests
 // writes one partial (O, M, l) for each of them, and a combine merges the
 // partials in closed form from the list. Ragged batches need no host
@@ -42,9 +47,10 @@ namespace sd {
 
 constexpr int kKaThreads = 256;
 constexpr int kKaWarps = kKaThreads / 32;
-constexpr int kKaTile = 16;      // tokens per warp and stage
+constexpr int kKaTile = 32;      // tokens per tile: one lookup per lane
+constexpr int kKaStep = 16;      // tokens per stage
 constexpr int kKaRanges = 296;   // CTAs of a column group in one wave: two per SM
-constexpr int kKaMinTiles = 2;   // fewest tiles a range gets (shorter lists use fewer ranges)
+constexpr int kKaMinTiles = 1;   // fewest tiles a range gets (shorter lists use fewer ranges)
 constexpr float kKaSlack = 8.f;  // log2: how far a weight may pass the running reference
 
 struct KvAttnArgs {
@@ -65,14 +71,21 @@ struct KvAttnArgs {
   float* lse;
 };
 
-template <int D, int NT>
+// HPW: query heads per warp (4, 8 or 16). Lane (n, t) of a fragment holds the
+// logits of tokens n and n + 8 for kHL heads.
+template <int D, int HPW, int TYPE>
 struct KvAttnCfg {
-  static constexpr int kHeads = 8 * NT;
-  static constexpr int kRowBytes = kKaTile * D;               // K (or V) of a stage
-  static constexpr int kStage = 2 * kRowBytes + 2 * kKaTile * 4;  // + the tokens' scales
+  static constexpr int kParts = TYPE == SD_KV_INT8 ? 3 : 2;
+  // HPW 4: column 2t + x of S tile j is part 2j + x of head t; else tile
+  // (hg, p) is part p of heads 8 hg .. 8 hg + 7
+  static constexpr int kSTiles = HPW == 4 ? (kParts + 1) / 2 : HPW / 8 * kParts;
+  static constexpr int kOTiles = HPW == 4 ? 1 : HPW / 8;
+  static constexpr int kHL = HPW == 4 ? 1 : HPW / 4;
+  static constexpr int kRowBytes = kKaStep * D;                   // K (or V) of a stage
+  static constexpr int kStage = 2 * kRowBytes + 2 * kKaStep * 4;  // + the tokens' scales
   static constexpr int kStages = D == 128 ? 3 : 5;
   static constexpr size_t kSmem = (size_t)kKaWarps * kStages * kStage;
-  static constexpr int kCtas = NT == 1 ? 2 : 1;               // resident CTAs per SM
+  static constexpr int kCtas = HPW == 16 ? 1 : 2;                 // resident CTAs per SM
 };
 
 // Tokens (dense) or list slots of request b that the attention walks.
@@ -95,6 +108,22 @@ __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// m16n8k32 over 8-bit operands; d is four int32 (int8) or fp32 (e4m3) sums.
+template <int TYPE>
+__device__ __forceinline__ void mma_8bit_16832(uint32_t* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (TYPE == SD_KV_INT8) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    float* f = reinterpret_cast<float*>(d);
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
@@ -103,6 +132,18 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+// 2^x and log2 x by the special-function unit (2^-22 relative, 2^-22 absolute
+// near one); results below fp32's normal range are zero.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Two codes in the low (HI = 0) or high half of w to fp16x2.
@@ -125,92 +166,108 @@ __device__ __forceinline__ uint32_t bias_codes(uint32_t w) {
   return TYPE == SD_KV_INT8 ? w ^ 0x80808080u : w;
 }
 
-// Exclusive position of the CTA's range in the tile list. All threads of the
-// CTA call it; `total` and the request that holds tile `first` come back in
-// every thread.
-__device__ __forceinline__ long long kv_attn_total(const KvAttnArgs& a, long long* s_sum, int threads) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Part p of four elements of q (already times the head's power of two).
+template <int TYPE>
+__device__ __forceinline__ uint32_t q_part(const float* x, int p) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (TYPE == SD_KV_INT8) {
+      int f = __float2int_rn(x[j]);  // |f| <= 2^22
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // digits from the low end: part 2, 1, 0
+        const int d = static_cast<int8_t>(f & 0xff);
+        if (p == 2 - i) w |= static_cast<uint32_t>(d & 0xff) << (8 * j);
+        f = (f - d) >> 8;
+      }
+      if (p == 0) w |= static_cast<uint32_t>(f & 0xff) << (8 * j);
+    } else {
+      const __nv_fp8_storage_t a = __nv_cvt_float_to_fp8(x[j], __NV_SATFINITE, __NV_E4M3);
+      const float rest = (x[j] - __half2float(__half(__nv_cvt_fp8_to_halfraw(a, __NV_E4M3)))) * 16.f;
+      const __nv_fp8_storage_t b = __nv_cvt_float_to_fp8(rest, __NV_SATFINITE, __NV_E4M3);
+      w |= static_cast<uint32_t>(p == 0 ? a : b) << (8 * j);
+    }
+  }
+  return w;
+}
+
+// Tiles of all requests, by one warp.
+__device__ __forceinline__ long long kv_attn_total(const KvAttnArgs& a) {
   long long n = 0;
-  for (int b = tid; b < a.B; b += threads) n += kv_attn_tiles(a, b);
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) n += kv_attn_tiles(a, b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  if (lane == 0) s_sum[warp] = n;
-  __syncthreads();
-  n = 0;
-  for (int w = 0; w < threads / 32; ++w) n += s_sum[w];
-  __syncthreads();
   return n;
 }
 
-template <int D, int NT, int TYPE, bool LIST>
-__global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, NT>::kCtas)) kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
-  using C = KvAttnCfg<D, NT>;
+// The request that holds tile t < total of the list, and its first tile, by
+// one warp.
+__device__ __forceinline__ int kv_attn_find(const KvAttnArgs& a, long long t, long long* first) {
+  const int lane = threadIdx.x & 31;
+  long long before = 0;
+  for (int base = 0;; base += 32) {
+    const int b = base + lane;
+    const int cnt = b < a.B ? kv_attn_tiles(a, b) : 0;
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const unsigned int past = __ballot_sync(0xffffffffu, before + incl > t);
+    if (past != 0 || base + 32 >= a.B) {
+      const int w = past != 0 ? __ffs(past) - 1 : 31;
+      *first = before + __shfl_sync(0xffffffffu, incl - cnt, w);
+      return min(base + w, a.B - 1);
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+template <int D, int HPW, int TYPE, bool LIST>
+__global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
+    kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
+  using C = KvAttnCfg<D, HPW, TYPE>;
   pdl_wait();  // inputs come from earlier work in the stream
   pdl_trigger();
 
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ long long s_sum[kKaWarps];
-  __shared__ long long s_first;
-  __shared__ int s_b;
   const KvGeom& geo = a.geo;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = lane >> 2, t = lane & 3;  // fragment coordinates
   const int G = geo.G;
 
-  // ---- this CTA's range of the tile list, and the request it starts in ----
-  const long long total = kv_attn_total(a, s_sum, kKaThreads);
+  // ---- this CTA's range of the tile list, and the request it starts in
+  // (every warp finds them for itself: no barrier) ----
+  const long long total = kv_attn_total(a);
   const int nr = kv_attn_ranges(a, total);
   if (blockIdx.x >= nr || total == 0) return;
   const long long t_begin = blockIdx.x * total / nr, t_end = (blockIdx.x + 1) * total / nr;
-  {
-    long long before = 0;
-    for (int base = 0; base < a.B; base += kKaThreads) {
-      const int b = base + tid;
-      const int cnt = b < a.B ? kv_attn_tiles(a, b) : 0;
-      long long incl = cnt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      if (lane == 31) s_sum[warp] = incl;
-      __syncthreads();
-      long long skip = before, all = 0;
-      for (int w = 0; w < kKaWarps; ++w) {
-        skip += w < warp ? s_sum[w] : 0;
-        all += s_sum[w];
-      }
-      const long long e = skip + incl;
-      if (t_begin < e && t_begin >= e - cnt) s_b = b, s_first = e - cnt;
-      before += all;
-      __syncthreads();
-      if (before > t_begin) break;
-    }
-  }
-  const int b_begin = s_b;
-  const int tile_begin = static_cast<int>(t_begin - s_first);
+  long long first;
+  const int b_begin = kv_attn_find(a, t_begin, &first);
+  const int tile_begin = static_cast<int>(t_begin - first);
 
   // ---- this warp's column ----
   const int col = a.cols >= kKaWarps ? blockIdx.y * kKaWarps + warp : warp % a.cols;
   const int sub = a.cols >= kKaWarps ? 0 : warp / a.cols;
-  if (col >= a.cols || sub >= a.spw) return;  // no barrier below
+  if (col >= a.cols || sub >= a.spw) return;
   const int hblocks = a.cols / G;
-  const int g = col / hblocks, h0 = g * a.qpk + (col % hblocks) * C::kHeads;
-  const int nh = min(C::kHeads, (g + 1) * a.qpk - h0);
+  const int g = col / hblocks, h0 = g * a.qpk + (col % hblocks) * HPW;
+  const int nh = min(HPW, (g + 1) * a.qpk - h0);
   unsigned char* ring = smem_raw + (size_t)warp * C::kStages * C::kStage;
-  const int my = static_cast<int>(t_end - t_begin);  // tiles, one stage each
+  const int my = 2 * static_cast<int>(t_end - t_begin);  // stages: two per tile
 
-  // ---- the copy side: three steps ahead of each other, so that a list
-  // entry, its page and its row are never waited for back to back ----
+  // ---- the copy side, one row per lane and tile, three steps ahead of each
+  // other, so that a list entry, its page and its row are never waited for
+  // back to back ----
   int pb = b_begin, ptile = tile_begin, plen = kv_attn_len(a, pb), pL = checked_seqlen(a.seqlens, pb, a.cap);
   int l1_tok = -1, l1_rem = 0, l1_b = 0, l1_L = 0;  // after step 1: list entry (or token)
-  int l2_page = -1, l2_slot = 0;                   // after step 2: page and slot
+  int l2_page = -1, l2_slot = 0;                    // after step 2: page and slot
   bool l2_ok = false;
-  const int r = lane & (kKaTile - 1);
   auto step1 = [&](bool live) {
     l1_tok = -1;
     if (!live) return;
-    const int v = (ptile * a.spw + sub) * kKaTile + r;
+    const int v = (ptile * a.spw + sub) * kKaTile + lane;
     l1_b = pb, l1_L = pL;
     if (v < plen) {
       if constexpr (LIST) {
@@ -258,43 +315,68 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, NT>::kCtas)) kv_attn
   constexpr int kRowsPerStep = 32 / kPieces;  // rows one copy instruction of the warp covers
   const int crow = lane / kPieces, cpiece = lane % kPieces;
   // swizzles: see the reads below
-  const int k_at = crow * D + ((D == 128 ? cpiece ^ ((crow & 1) << 2) : cpiece) << 4);
-  const int v_at = crow * D + ((D == 128 ? cpiece ^ ((crow & 3) << 1) : cpiece ^ (((crow >> 1) & 1) << 1)) << 4);
-  auto issue = [&](int stage) {
-    unsigned char* st = ring + stage * C::kStage;
-    int rid = -1;
+  const uint32_t ring_at = smem_u32(ring);
+  const uint32_t k_at = ring_at + crow * D + ((D == 128 ? cpiece ^ ((crow & 1) << 2) : cpiece) << 4);
+  const uint32_t v_at = ring_at + C::kRowBytes + crow * D +
+                        ((D == 128 ? cpiece ^ ((crow & 3) << 1) : cpiece ^ (((crow >> 1) & 1) << 1)) << 4);
+  const uint8_t* k_src = a.k_pages + cpiece * 16;
+  const uint8_t* v_src = a.v_pages + cpiece * 16;
+  uint32_t row16 = 0;   // this lane's row of the current tile, in 16-byte units; ~0: no token
+  long long scale_at = 0;
+  auto resolve = [&]() {
+    row16 = ~0u;
     if (l2_ok) {
-      if (l2_page >= 0 && l2_page < geo.num_pages) rid = l2_page * geo.page_size + l2_slot;
-      else raise_error(SD_DEVERR_PAGE);
+      if (l2_page >= 0 && l2_page < geo.num_pages) {
+        const int rid = l2_page * geo.page_size + l2_slot;
+        row16 = (static_cast<uint32_t>(rid) * G + g) * kPieces;
+        scale_at = (long long)geo.bs_div.div(rid) * G + g;
+      } else {
+        raise_error(SD_DEVERR_PAGE);
+      }
     }
+  };
+  auto issue = [&](int stage, int half) {
+    const uint32_t off = stage * C::kStage;
+    const bool whole = __all_sync(0xffffffffu, row16 != ~0u);
 #pragma unroll
-    for (int j = 0; j < kKaTile / kRowsPerStep; ++j) {
-      const int row = __shfl_sync(0xffffffffu, rid, crow + j * kRowsPerStep);
-      const long long off = ((long long)max(row, 0) * G + g) * D + cpiece * 16;
-      const int bytes = row >= 0 ? 16 : 0;  // 0: the piece is filled with zeros
-      cp_async_16(st + k_at + j * kRowsPerStep * D, a.k_pages + off, bytes);
-      cp_async_16(st + C::kRowBytes + v_at + j * kRowsPerStep * D, a.v_pages + off, bytes);
+    for (int j = 0; j < kKaStep / kRowsPerStep; ++j) {
+      uint32_t row = __shfl_sync(0xffffffffu, row16, half * kKaStep + crow + j * kRowsPerStep);
+      int bytes = 16;
+      if (!whole) {  // 0 bytes: the piece is filled with zeros
+        bytes = row != ~0u ? 16 : 0;
+        row = row != ~0u ? row : 0u;
+      }
+      const size_t at = (size_t)row * 16;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(k_at + off + j * kRowsPerStep * D), "l"(k_src + at), "r"(bytes)
+                   : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(v_at + off + j * kRowsPerStep * D), "l"(v_src + at), "r"(bytes)
+                   : "memory");
     }
-    float* sc = reinterpret_cast<float*>(st + 2 * C::kRowBytes) + lane;  // lanes 0-15: K, 16-31: V
-    if (rid >= 0) {
-      const float* src = (lane < kKaTile ? a.k_scales : a.v_scales) + (long long)geo.bs_div.div(rid) * G + g;
-      cp_async_4(sc, src);
-    } else {
-      *sc = -1.f;  // no token here
+    if (lane / kKaStep == half) {
+      float* sc = reinterpret_cast<float*>(ring + off + 2 * C::kRowBytes) + lane % kKaStep;
+      if (row16 != ~0u) {
+        cp_async_4(sc, a.k_scales + scale_at);
+        cp_async_4(sc + kKaStep, a.v_scales + scale_at);
+      } else {
+        sc[0] = -1.f;  // no token here
+        sc[kKaStep] = 1.f;
+      }
     }
   };
 
   // ---- the compute side ----
-  int cb = b_begin, ctile = tile_begin;
-  int cntiles = kv_attn_tiles(a, cb);
-  uint32_t qf[NT][D / 16][2];
-  float qs[NT][2];                     // scale of heads 2t, 2t + 1 (base-2 logits)
-  float o[NT][D / 16][4];
-  float m[NT][2], l[NT][2];
+  int cb = b_begin, ctile = tile_begin, clen = kv_attn_len(a, cb);
+  uint32_t qf[C::kSTiles][D / 32][2];
+  float qs[C::kHL];  // scale of this lane's heads (base-2 logits)
+  float o[C::kOTiles][D / 16][4];
+  float m[C::kHL], l[C::kHL];
+  // head of this lane's logits, and of column n of S tile j (its part too)
+  auto lane_head = [&](int i) { return HPW == 4 ? t : (i >> 1) * 8 + 2 * t + (i & 1); };
   auto load_q = [&]() {
+    float back_of[C::kOTiles];  // scale of head n (HPW 4: n / 2) of head group j
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int h = i * 8 + n;
+    for (int hg = 0; hg < C::kOTiles; ++hg) {
+      const int h = HPW == 4 ? n >> 1 : hg * 8 + n;
       const __nv_bfloat16* src = a.q + ((size_t)cb * a.H + h0 + (h < nh ? h : 0)) * D;
       uint4 raw[D / 32];
 #pragma unroll
@@ -304,158 +386,184 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, NT>::kCtas)) kv_attn
       }
       const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
       float amax = 0.f;
+      bool bad = false;
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
         const float2 x = bf2(w[j]);
         amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+        bad |= !(fabsf(x.x) <= FLT_MAX) || !(fabsf(x.y) <= FLT_MAX);
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // up = 2^(14 - floor(log2 amax)), as two factors since it can pass 2^127
+      // up = 2^(e - floor(log2 amax)), as two factors since it can pass 2^127
       int ex = static_cast<int>(__float_as_uint(amax) >> 23);  // biased; 0: zero or subnormal
       ex = min(max(ex, 1), 254);
-      const int up = 14 + 127 - ex;                            // -113 .. 140
+      const int up = (TYPE == SD_KV_INT8 ? 21 : 7) + 127 - ex;
       const float f0 = __uint_as_float((uint32_t)(up / 2 + 127) << 23), f1 = __uint_as_float((uint32_t)(up - up / 2 + 127) << 23);
-      const float back = a.scale_log2 / f0 / f1;
+      back_of[hg] = a.scale_log2 / f0 / f1;
+      // a query that is not finite makes its head's output NaN
+      if (__shfl_xor_sync(0xffffffffu, bad, 1) || bad) bad = true;
+      if (__shfl_xor_sync(0xffffffffu, bad, 2) || bad) back_of[hg] = __uint_as_float(0x7fc00000u);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
+      for (int kk = 0; kk < D / 16; ++kk) {  // word kk: dims of K's word kk
         const float2 x = bf2(w[2 * kk]), y = bf2(w[2 * kk + 1]);
-        qf[i][kk][0] = pack_half2(x.x * f0 * f1, x.y * f0 * f1);
-        qf[i][kk][1] = pack_half2(y.x * f0 * f1, y.y * f0 * f1);
-      }
-      qs[i][0] = __shfl_sync(0xffffffffu, back, (2 * t) * 4);
-      qs[i][1] = __shfl_sync(0xffffffffu, back, (2 * t + 1) * 4);
-      m[i][0] = m[i][1] = -INFINITY;
-      l[i][0] = l[i][1] = 0.f;
+        const float e[4] = {x.x * f0 * f1, x.y * f0 * f1, y.x * f0 * f1, y.y * f0 * f1};
+        if constexpr (HPW == 4) {
+          const uint32_t p0 = q_part<TYPE>(e, 0), p1 = q_part<TYPE>(e, 1);
+          qf[0][kk / 2][kk % 2] = n & 1 ? p1 : p0;
+          if constexpr (C::kSTiles == 2) qf[1][kk / 2][kk % 2] = n & 1 ? 0u : q_part<TYPE>(e, 2);
+        } else {
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+          for (int p = 0; p < C::kParts; ++p) qf[hg * C::kParts + p][kk / 2][kk % 2] = q_part<TYPE>(e, p);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) o[hg][j][0] = o[hg][j][1] = o[hg][j][2] = o[hg][j][3] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < C::kHL; ++i) {
+      qs[i] = __shfl_sync(0xffffffffu, back_of[HPW == 4 ? 0 : i >> 1], (HPW == 4 ? 2 * t : 2 * t + (i & 1)) * 4);
+      m[i] = -INFINITY;
+      l[i] = 0.f;
     }
   };
   auto flush = [&]() {
     const size_t slot = ((size_t)blockIdx.x + cb) * a.spw + sub;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < C::kHL; ++i) {
+      float s = l[i];
+      s += __shfl_xor_sync(0xffffffffu, s, 4);
+      s += __shfl_xor_sync(0xffffffffu, s, 8);
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+      const int h = lane_head(i);
+      if (h >= nh) continue;
+      const size_t at = slot * a.H + h0 + h;
+      if (n == 0) a.part_ml[at] = make_float2(m[i], s);
+      // this lane's dims of the head: n * D/8 .. + D/8 - 1, dim 2j and 2j + 1 from m-tile j
+      float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + n * (D / 8));
+      const int hg = HPW == 4 ? 0 : i >> 1, x = HPW == 4 ? 0 : i & 1;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float s = l[i][x];
-        s += __shfl_xor_sync(0xffffffffu, s, 4);
-        s += __shfl_xor_sync(0xffffffffu, s, 8);
-        s += __shfl_xor_sync(0xffffffffu, s, 16);
-        const int h = i * 8 + 2 * t + x;
-        if (h >= nh) continue;
-        const size_t at = slot * a.H + h0 + h;
-        if (n == 0) a.part_ml[at] = make_float2(m[i][x], s);
-        // this lane's dims of the head: n * D/8 .. + D/8 - 1, dim 2j and 2j + 1 from m-tile j
-        float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + n * (D / 8));
-#pragma unroll
-        for (int j = 0; j < D / 16; j += 2)
-          dst[j / 2] = make_float4(o[i][j][x], o[i][j][2 + x], o[i][j + 1][x], o[i][j + 1][2 + x]);
-      }
+      for (int j = 0; j < D / 16; j += 2)
+        dst[j / 2] = make_float4(o[hg][j][x], o[hg][j][2 + x], o[hg][j + 1][x], o[hg][j + 1][2 + x]);
     }
   };
 
-  // A row i (= n, n + 8) of the token tile is token pi(i): pi(2j) = j,
+  // A row i (= n, n + 8) of the stage is token pi(i): pi(2j) = j,
   // pi(2j + 1) = (j + 4) ^ 1, + 8 for the upper half. It makes the rows that one
   // phase of a shared load touches differ in the bits the swizzles use.
   const int tk = (n & 1) ? (((n >> 1) + 4) ^ 1) : (n >> 1);
   const int tv0 = t, tv1 = (t + 4) ^ 1;  // tokens pi(2t), pi(2t + 1)
 
+  // stage i is half i & 1 of tile i / 2; its tile is resolved when half 0 is issued
+  auto feed = [&](int i, int stage) {
+    if (i < my) {
+      if ((i & 1) == 0) {
+        resolve();
+        step2();
+        step1(i + 4 < my);
+      }
+      issue(stage, i & 1);
+    }
+    cp_async_commit();
+  };
   step1(my > 0);
   step2();
-  step1(my > 1);
+  step1(my > 2);
 #pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) {
-    if (s < my) issue(s);
-    cp_async_commit();
-    step2();
-    step1(s + 2 < my);
-  }
+  for (int s = 0; s < C::kStages - 1; ++s) feed(s, s);
   load_q();
   int stage = 0;
-  for (int i = 0; i < my; ++i) {
+  for (int at = 0; at < my; ++at) {
     cp_async_wait<C::kStages - 2>();
     __syncwarp();
-    {
-      int st = stage + C::kStages - 1;
-      if (st >= C::kStages) st -= C::kStages;
-      if (i + C::kStages - 1 < my) issue(st);
-      cp_async_commit();
-      step2();
-      step1(i + C::kStages + 1 < my);
-    }
+    feed(at + C::kStages - 1, stage == 0 ? C::kStages - 1 : stage - 1);
     const unsigned char* sk = ring + stage * C::kStage;
     const unsigned char* sv = sk + C::kRowBytes;
     const float* sc = reinterpret_cast<const float*>(sv + C::kRowBytes);
 
-    // ---- S^T = K Q^T: 16 tokens x 8 NT heads ----
-    float s[NT][4];
+    // ---- S^T = K Q^T: 16 tokens x (heads and parts) ----
+    uint32_t s[C::kSTiles][4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+    for (int j = 0; j < C::kSTiles; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0u;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       const int piece = D == 128 ? (t + 4 * j) ^ ((tk & 1) << 2) : t;
       const uint4 x = *reinterpret_cast<const uint4*>(sk + tk * D + piece * 16);
       const uint4 y = *reinterpret_cast<const uint4*>(sk + (tk + 8) * D + piece * 16);
-      const uint32_t* xw = reinterpret_cast<const uint32_t*>(&x);
-      const uint32_t* yw = reinterpret_cast<const uint32_t*>(&y);
+      const uint32_t f0[4] = {x.x, y.x, x.y, y.y}, f1[4] = {x.z, y.z, x.w, y.w};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t xb = bias_codes<TYPE>(xw[w]), yb = bias_codes<TYPE>(yw[w]);
-        const uint32_t af[4] = {codes_to_half2<TYPE, 0>(xb), codes_to_half2<TYPE, 0>(yb), codes_to_half2<TYPE, 1>(xb),
-                                codes_to_half2<TYPE, 1>(yb)};
-#pragma unroll
-        for (int h = 0; h < NT; ++h) mma_f16_16816(s[h], af, qf[h][4 * j + w][0], qf[h][4 * j + w][1]);
+      for (int h = 0; h < C::kSTiles; ++h) {
+        mma_8bit_16832<TYPE>(s[h], f0, qf[h][2 * j][0], qf[h][2 * j][1]);
+        mma_8bit_16832<TYPE>(s[h], f1, qf[h][2 * j + 1][0], qf[h][2 * j + 1][1]);
       }
     }
 
-    // ---- weights ----
-    const float sk0 = sc[tk], sk1 = sc[tk + 8];
-    const float lv0 = log2f(fmaxf(sc[kKaTile + tk], FLT_MIN)), lv1 = log2f(fmaxf(sc[kKaTile + tk + 8], FLT_MIN));
-    const bool ok0 = sk0 >= 0.f, ok1 = sk1 >= 0.f;
+    // ---- weights of tokens n and n + 8 ----
+    float w[2][C::kHL];
     bool over = false;
+    float isv[2];
 #pragma unroll
-    for (int h = 0; h < NT; ++h) {
+    for (int r = 0; r < 2; ++r) {
+      const float ks = sc[tk + 8 * r], vs = fmaxf(sc[kKaStep + tk + 8 * r], FLT_MIN);
+      const float lv = fast_log2(vs);
+      isv[r] = __fdividef(1.f, vs);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        s[h][x] = ok0 ? s[h][x] * (qs[h][x] * sk0) : -INFINITY;
-        s[h][2 + x] = ok1 ? s[h][2 + x] * (qs[h][x] * sk1) : -INFINITY;
-        over |= s[h][x] + lv0 > m[h][x] + kKaSlack || s[h][2 + x] + lv1 > m[h][x] + kKaSlack;
+      for (int i = 0; i < C::kHL; ++i) {
+        // the parts of this lane's head i
+        float z;
+        if constexpr (HPW == 4) {
+          if constexpr (TYPE == SD_KV_INT8)
+            z = fmaf(static_cast<float>(static_cast<int>(s[0][2 * r]) * 256 + static_cast<int>(s[0][2 * r + 1])), 256.f,
+                     static_cast<float>(static_cast<int>(s[1][2 * r])));
+          else
+            z = fmaf(__uint_as_float(s[0][2 * r + 1]), 0.0625f, __uint_as_float(s[0][2 * r]));
+        } else {
+          const uint32_t(*p)[4] = s + (i >> 1) * C::kParts;
+          const int x = 2 * r + (i & 1);
+          if constexpr (TYPE == SD_KV_INT8)
+            z = fmaf(static_cast<float>(static_cast<int>(p[0][x]) * 256 + static_cast<int>(p[1][x])), 256.f,
+                     static_cast<float>(static_cast<int>(p[2][x])));
+          else
+            z = fmaf(__uint_as_float(p[1][x]), 0.0625f, __uint_as_float(p[0][x]));
+        }
+        w[r][i] = ks >= 0.f ? fmaf(z, qs[i] * ks, lv) : -INFINITY;  // u
+        over |= w[r][i] > m[i] + kKaSlack;
       }
     }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-      for (int h = 0; h < NT; ++h) {
+      for (int i = 0; i < C::kHL; ++i) {
+        float mx = fmaxf(w[0][i], w[1][i]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        mx = fmaxf(mx, m[i]);
+        const float alpha = mx == -INFINITY ? 1.f : fast_exp2(m[i] - mx);
+        m[i] = mx;
+        l[i] *= alpha;
+        const int hg = HPW == 4 ? 0 : i >> 1, x = HPW == 4 ? 0 : i & 1;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float mx = fmaxf(s[h][x] + lv0, s[h][2 + x] + lv1);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          mx = fmaxf(mx, m[h][x]);
-          const float alpha = mx == -INFINITY ? 1.f : exp2f(m[h][x] - mx);
-          m[h][x] = mx;
-          l[h][x] *= alpha;
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) o[h][j][x] *= alpha, o[h][j][2 + x] *= alpha;
-        }
+        for (int j = 0; j < D / 16; ++j) o[hg][j][x] *= alpha, o[hg][j][2 + x] *= alpha;
       }
     }
-    uint32_t pf[NT][2];
 #pragma unroll
-    for (int h = 0; h < NT; ++h) {
-      float w[4];
+    for (int i = 0; i < C::kHL; ++i) {
+      const float ref = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float ref = m[h][x] == -INFINITY ? 0.f : m[h][x];
-        l[h][x] += exp2f(s[h][x] - ref) + exp2f(s[h][2 + x] - ref);
-        w[x] = exp2f(s[h][x] + lv0 - ref);
-        w[2 + x] = exp2f(s[h][2 + x] + lv1 - ref);
+      for (int r = 0; r < 2; ++r) {
+        w[r][i] = fast_exp2(w[r][i] - ref);
+        l[i] = fmaf(w[r][i], isv[r], l[i]);
       }
-      pf[h][0] = transpose_8x8(pack_half2(w[0], w[1]));
-      pf[h][1] = transpose_8x8(pack_half2(w[2], w[3]));
+    }
+    uint32_t pf[C::kOTiles][2];
+#pragma unroll
+    for (int h = 0; h < C::kOTiles; ++h) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        pf[h][r] = transpose_8x8(HPW == 4 ? pack_half2(w[r][0], 0.f) : pack_half2(w[r][2 * h], w[r][(2 * h + 1) % C::kHL]));
     }
 
-    // ---- O^T += V^T P^T: D dims x 8 NT heads; lane row n holds dims
+    // ---- O^T += V^T P^T: D dims x heads; lane row n holds dims
     // n * D/8 .. n * D/8 + D/8 - 1 of the tokens tv0, tv1 (+ 8) ----
     constexpr int kVW = D / 32;  // 4-byte words of a lane's part of a V row
     uint32_t va[4][kVW];
@@ -471,31 +579,33 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, NT>::kCtas)) kv_attn
       }
     }
 #pragma unroll
-    for (int w = 0; w < kVW; ++w) {
+    for (int v = 0; v < kVW; ++v) {
       // bytes of two tokens side by side: (tok0 dim d, tok1 dim d), ...
-      const uint32_t x0 = bias_codes<TYPE>(__byte_perm(va[0][w], va[1][w], 0x5140));
-      const uint32_t x1 = bias_codes<TYPE>(__byte_perm(va[0][w], va[1][w], 0x7362));
-      const uint32_t y0 = bias_codes<TYPE>(__byte_perm(va[2][w], va[3][w], 0x5140));
-      const uint32_t y1 = bias_codes<TYPE>(__byte_perm(va[2][w], va[3][w], 0x7362));
+      const uint32_t x0 = bias_codes<TYPE>(__byte_perm(va[0][v], va[1][v], 0x5140));
+      const uint32_t x1 = bias_codes<TYPE>(__byte_perm(va[0][v], va[1][v], 0x7362));
+      const uint32_t y0 = bias_codes<TYPE>(__byte_perm(va[2][v], va[3][v], 0x5140));
+      const uint32_t y1 = bias_codes<TYPE>(__byte_perm(va[2][v], va[3][v], 0x7362));
       const uint32_t f0[4] = {codes_to_half2<TYPE, 0>(x0), codes_to_half2<TYPE, 1>(x0), codes_to_half2<TYPE, 0>(y0),
                               codes_to_half2<TYPE, 1>(y0)};
       const uint32_t f1[4] = {codes_to_half2<TYPE, 0>(x1), codes_to_half2<TYPE, 1>(x1), codes_to_half2<TYPE, 0>(y1),
                               codes_to_half2<TYPE, 1>(y1)};
 #pragma unroll
-      for (int h = 0; h < NT; ++h) {
-        mma_f16_16816(o[h][2 * w], f0, pf[h][0], pf[h][1]);
-        mma_f16_16816(o[h][2 * w + 1], f1, pf[h][0], pf[h][1]);
+      for (int h = 0; h < C::kOTiles; ++h) {
+        mma_f16_16816(o[h][2 * v], f0, pf[h][0], pf[h][1]);
+        mma_f16_16816(o[h][2 * v + 1], f1, pf[h][0], pf[h][1]);
       }
     }
 
     if (++stage == C::kStages) stage = 0;
-    if (++ctile == cntiles || i + 1 == my) {  // the request or the range ends
-      flush();
-      if (i + 1 < my) {
-        ctile = 0;
-        do cntiles = kv_attn_tiles(a, ++cb);
-        while (cntiles == 0 && cb + 1 < a.B);
-        load_q();
+    if (at & 1) {
+      if ((++ctile) * a.spw * kKaTile >= clen || at + 1 == my) {  // the request or the range ends
+        flush();
+        if (at + 1 < my) {
+          ctile = 0;
+          do clen = kv_attn_len(a, ++cb);
+          while (clen == 0 && cb + 1 < a.B);
+          load_q();
+        }
       }
     }
   }
@@ -504,71 +614,85 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, NT>::kCtas)) kv_attn
 
 // Merges the partials of one (request, query head): with M = max M_i,
 // o = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i. One CTA each; a group of
-// D / 4 lanes takes every (128 / (D / 4))-th partial.
-constexpr int kKaCombineThreads = 128;
+// D / 4 lanes takes every GROUPS-th partial, a batch of them in flight
+// together with their (M, l), and keeps a running maximum: one trip to L2
+// for up to kKaBatch * GROUPS partials. The list is walked before the wait for the
+// attention.
+constexpr int kKaCombineThreads = 256;
+constexpr int kKaBatch = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kKaCombineThreads) kv_attn_combine_kernel(const __grid_constant__ KvAttnArgs a) {
   constexpr int LANES = D / 4, GROUPS = kKaCombineThreads / LANES;
-  __shared__ long long s_sum[kKaCombineThreads / 32];
-  __shared__ float s_m[kKaCombineThreads / 32];
-  __shared__ float s_l[GROUPS];
+  __shared__ float2 s_ml[GROUPS];
   __shared__ float4 s_o[GROUPS][LANES];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int tid = threadIdx.x;
+  const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
   // the caller's lengths: no kernel of this call writes them, and this kernel
   // starts only after the attention has passed its own wait
-  const long long total = kv_attn_total(a, s_sum, kKaCombineThreads);
+  const long long total = kv_attn_total(a);
   long long first = 0;
-  for (int i = tid; i < b; i += kKaCombineThreads) first += kv_attn_tiles(a, i);
+  for (int i = tid & 31; i < b; i += 32) first += kv_attn_tiles(a, i);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-  if (lane == 0) s_sum[warp] = first;
-  __syncthreads();
-  first = 0;
-  for (int w = 0; w < kKaCombineThreads / 32; ++w) first += s_sum[w];
   const int tiles = kv_attn_tiles(a, b);
+  const size_t bh = (size_t)b * a.H + h;
+  const int grp = tid / LANES, ln = tid % LANES;
+  int parts = 0;
+  size_t slot0 = 0;
+  if (tiles > 0) {
+    const int nr = kv_attn_ranges(a, total);
+    const long long r0 = ((first + 1) * nr - 1) / total, r1 = ((first + tiles) * nr - 1) / total;
+    parts = static_cast<int>(r1 - r0 + 1) * a.spw;
+    slot0 = (size_t)(r0 + b) * a.spw;
+  }
   pdl_wait();
   pdl_trigger();
-  const size_t bh = (size_t)b * a.H + h;
-  if (tiles == 0) {
-    if (tid < LANES) *reinterpret_cast<uint2*>(a.out + bh * D + 4 * tid) = make_uint2(0u, 0u);
-    if (a.lse != nullptr && tid == 0) a.lse[bh] = -INFINITY;
-    return;
-  }
-  const int nr = kv_attn_ranges(a, total);
-  const long long r0 = ((first + 1) * nr - 1) / total, r1 = ((first + tiles) * nr - 1) / total;
-  const int parts = static_cast<int>(r1 - r0 + 1) * a.spw;
-  const size_t slot0 = (size_t)(r0 + b) * a.spw;
-  float M = -INFINITY;
-  for (int i = tid; i < parts; i += kKaCombineThreads) M = fmaxf(M, a.part_ml[(slot0 + i) * a.H + h].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_m[warp] = M;
-  __syncthreads();
-  for (int w = 0; w < kKaCombineThreads / 32; ++w) M = fmaxf(M, s_m[w]);
-  const int grp = tid / LANES, ln = tid % LANES;
-  float l = 0.f;
+  float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = grp; i < parts; i += GROUPS) {
-    const size_t at = (slot0 + i) * a.H + h;
-    const float2 ml = a.part_ml[at];
-    const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * D + 4 * ln);
-    const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - M);  // sum 0: no token there
-    l += f * ml.y;
-    acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+  for (int i0 = grp; i0 < parts; i0 += GROUPS * kKaBatch) {
+    float2 ml[kKaBatch];
+    float4 x[kKaBatch];
+#pragma unroll
+    for (int j = 0; j < kKaBatch; ++j) {
+      const int i = i0 + j * GROUPS;
+      ml[j] = make_float2(-INFINITY, 0.f);
+      x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < parts) {
+        const size_t at = (slot0 + i) * a.H + h;
+        ml[j] = a.part_ml[at];
+        x[j] = *reinterpret_cast<const float4*>(a.part_o + at * D + 4 * ln);
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int j = 0; j < kKaBatch; ++j) m = fmaxf(m, ml[j].x);
+    const float back = M == -INFINITY ? 0.f : exp2f(M - m);
+    M = m;
+    l *= back;
+    acc.x *= back, acc.y *= back, acc.z *= back, acc.w *= back;
+#pragma unroll
+    for (int j = 0; j < kKaBatch; ++j) {
+      const float f = ml[j].y == 0.f ? 0.f : exp2f(ml[j].x - m);  // sum 0: no token there
+      l += f * ml[j].y;
+      acc.x += f * x[j].x, acc.y += f * x[j].y, acc.z += f * x[j].z, acc.w += f * x[j].w;
+    }
   }
   s_o[grp][ln] = acc;
-  if (ln == 0) s_l[grp] = l;
+  if (ln == 0) s_ml[grp] = make_float2(M, l);
   __syncthreads();
   if (tid >= LANES) return;
+#pragma unroll
+  for (int i = 0; i < GROUPS; ++i) M = fmaxf(M, s_ml[i].x);
   l = 0.f;
   acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
   for (int i = 0; i < GROUPS; ++i) {
+    const float2 ml = s_ml[i];
     const float4 x = s_o[i][ln];
-    l += s_l[i];
-    acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+    const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
+    l += f * ml.y;
+    acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: nothing was attended
   *reinterpret_cast<uint2*>(a.out + bh * D + 4 * ln) =

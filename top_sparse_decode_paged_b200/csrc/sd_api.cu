@@ -1001,17 +1001,17 @@ sd::KvGeom kv_geom(const sd_kv_cache& kv, const sd_paged_desc& pd) {
 
 // How the attention over 8-bit pools is cut up: a function of the shape only.
 struct KvAttnPlan {
-  int nt, cols, col_groups, spw, ranges;
+  int hpw, cols, col_groups, spw, ranges;
   size_t off_ml, total;
 };
 KvAttnPlan kv_attn_plan(int B, int G, int H, int D) {
   KvAttnPlan p{};
   const int qpk = H / G;
-  p.nt = qpk > 8 ? 2 : 1;  // 16 query heads share a warp's unpacked K and V above 8 per KV head
-  p.cols = G * sd::ceil_div(qpk, 8 * p.nt);
+  p.hpw = qpk <= 4 ? 4 : qpk <= 8 ? 8 : 16;  // query heads that share a warp's K and V
+  p.cols = G * sd::ceil_div(qpk, p.hpw);
   p.col_groups = sd::ceil_div(p.cols, sd::kKaWarps);
   p.spw = p.cols >= sd::kKaWarps ? 1 : sd::kKaWarps / p.cols;
-  p.ranges = std::max(1, sd::kKaRanges / (p.nt == 2 ? 2 : 1) / p.col_groups);
+  p.ranges = std::max(1, sd::kKaRanges / (p.hpw == 16 ? 2 : 1) / p.col_groups);
   const size_t rows = ((size_t)p.ranges + B) * p.spw * H;
   p.off_ml = align_up(rows * D * sizeof(float));
   p.total = p.off_ml + align_up(rows * sizeof(float2));
@@ -1024,14 +1024,16 @@ sd_status check_kv_attn_args(const uint16_t* q, const sd_kv_cache& kv, const int
   if (s != SD_OK) return s;
   if (B < 0 || H <= 0 || H % pd.kv_heads != 0 || !isfinite(scale)) return SD_ERR_INVALID_ARG;
   if (B > 0 && (!q || !bt || !seqlens || !out || !aligned(q, 16) || !aligned(out, 8))) return SD_ERR_INVALID_ARG;
+  // rows are addressed in 16-byte units held in 32 bits: pools up to 64 GiB
+  if ((unsigned long long)pd.num_pages * pd.page_size * pd.kv_heads * kv.D >= (1ull << 36) - 16) return SD_ERR_UNSUPPORTED;
   if (kv.kv_type == SD_KV_BF16 || H / pd.kv_heads > 128 || (long long)B * H >= (1ll << 31)) return SD_ERR_UNSUPPORTED;
   return SD_OK;
 }
 
-template <int D, int NT, int TYPE, bool LIST>
+template <int D, int HPW, int TYPE, bool LIST>
 sd_status launch_kv_attn_t(const sd::KvAttnArgs& a, cudaStream_t st) {
-  auto kern = sd::kv_attn_kernel<D, NT, TYPE, LIST>;
-  constexpr size_t smem = sd::KvAttnCfg<D, NT>::kSmem;
+  auto kern = sd::kv_attn_kernel<D, HPW, TYPE, LIST>;
+  constexpr size_t smem = sd::KvAttnCfg<D, HPW, TYPE>::kSmem;
   const sd_status s = set_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (s != SD_OK) return s;
   return launch_k(kern, dim3(a.ranges, a.col_groups), dim3(sd::kKaThreads), smem, st, a);
@@ -1070,15 +1072,15 @@ sd_status launch_kv_attn(const uint16_t* q, const sd_kv_cache& kv, const int32_t
   a.lse = lse;
   sd_status s = SD_OK;
   stage_mark(kStageAttn, 0, st);
-#define SD_KA(D_, NT_)                                                                                        \
-  s = kv.kv_type == SD_KV_INT8 ? (indices ? launch_kv_attn_t<D_, NT_, SD_KV_INT8, true>(a, st)                \
-                                          : launch_kv_attn_t<D_, NT_, SD_KV_INT8, false>(a, st))              \
-                               : (indices ? launch_kv_attn_t<D_, NT_, SD_KV_E4M3, true>(a, st)                \
-                                          : launch_kv_attn_t<D_, NT_, SD_KV_E4M3, false>(a, st))
+#define SD_KA(D_, HPW_)                                                                                       \
+  s = kv.kv_type == SD_KV_INT8 ? (indices ? launch_kv_attn_t<D_, HPW_, SD_KV_INT8, true>(a, st)               \
+                                          : launch_kv_attn_t<D_, HPW_, SD_KV_INT8, false>(a, st))             \
+                               : (indices ? launch_kv_attn_t<D_, HPW_, SD_KV_E4M3, true>(a, st)               \
+                                          : launch_kv_attn_t<D_, HPW_, SD_KV_E4M3, false>(a, st))
   if (kv.D == 64) {
-    if (p.nt == 1) SD_KA(64, 1); else SD_KA(64, 2);
+    if (p.hpw == 4) SD_KA(64, 4); else if (p.hpw == 8) SD_KA(64, 8); else SD_KA(64, 16);
   } else {
-    if (p.nt == 1) SD_KA(128, 1); else SD_KA(128, 2);
+    if (p.hpw == 4) SD_KA(128, 4); else if (p.hpw == 8) SD_KA(128, 8); else SD_KA(128, 16);
   }
 #undef SD_KA
   stage_mark(kStageAttn, 1, st);
