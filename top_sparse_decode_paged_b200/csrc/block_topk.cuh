@@ -6,18 +6,25 @@
 // library's top-k takes the best others, ties to the lower block.
 //
 // The sums are held in fp64, where a product of two bf16 values is exact and
-// the sum is wrong by 2^-46 of its terms at most, and rounded once to fp32: which blocks are
-// selected does not depend on the order of the sum. max(q lo, q hi) = max(q, 0) hi +
-// min(q, 0) lo, two fused multiply-adds without a select. A bf16 value becomes
-// a double by moving its bits: (x >> 3) with the sign kept, as the high word, is
-// x * 2^-896 for every finite x, subnormals and zero included; q carries 2^800 and the
-// result 2^96 to make up for it.
+// the sum is wrong by 2^-46 of its terms at most, and rounded once to fp32:
+// which blocks are selected does not depend on the order of the sum.
+// max(q lo, q hi) is q times one of the two, picked by q's sign. A bf16 value
+// becomes a double by moving its bits: (x >> 3) with the sign kept, as the
+// high word, is x * 2^-896 for every finite x, subnormals and zero included;
+// q carries 2^800 and the result 2^96 to make up for it.
 //
-// Split: one warp per 32 blocks of a (request, KV head), a block per lane, so
-// that q is uniform over the warp and the sums need no shuffle; the blocks'
-// bounds are staged in shared memory with cp.async. Bound by HBM (4 D bytes
-// per block and KV head) up to four query heads per KV head, and by the fp64
-// pipe above.
+// Split of the scores: D / 4 lanes share a block, four dims each, so that a
+// lane keeps its dims of four query heads in registers and reads the bounds
+// straight from global memory; the sums of four blocks and four heads are
+// reduced over the lanes together, halving their number at each step. Bound
+// by HBM (4 D bytes per block and KV head) up to four query heads per KV
+// head, and by issue slots above.
+//
+// block_select_kernel: one CTA per (request, KV head) row of up to
+// kBsMaxBlocks keys, held in registers. A histogram of the 11 bits below the
+// highest differing bit gives the digit of the last key to take; its few
+// keys are ranked directly (further digits where they are many). Longer rows
+// take the library's cluster top-k. Bound by its chain of barriers.
 #pragma once
 
 #include "kv_store.cuh"
@@ -27,122 +34,315 @@ namespace sd {
 
 constexpr int kBtWarps = 4;
 constexpr int kBtThreads = 32 * kBtWarps;
-constexpr int kBtBlocks = 32;  // blocks per warp
-constexpr int kBtHeads = 4;    // query heads summed at once
+constexpr int kBtHeads = 4;   // query heads summed at once
+constexpr int kBtBatch = 4;   // blocks a lane group has in flight
+constexpr int kBtChunk = 32;  // most blocks per warp
 
 struct BlockScoreArgs {
   const __nv_bfloat16 *q, *bounds;
   const int32_t *block_table, *seqlens;
   KvGeom geo;
   int B, H, qpk, max_blocks, cap, n_first, n_last;
+  int chunk;        // blocks per warp
   int32_t* keys;    // [B, G, max_blocks] order-preserving
   int32_t* counts;  // [B] blocks of each request
 };
 
-template <int D>
-struct BlockScoreCfg {
-  static constexpr int kRow = 4 * D + 16;  // one block's bounds, padded: 16-byte reads of 8 lanes hit all banks
-  static constexpr size_t kSmem = (size_t)kBtWarps * kBtBlocks * kRow;
-};
-
-// x * 2^-896 from the bits of the bf16 in the low or high half of w.
-__device__ __forceinline__ double bf16_lo_to_scaled(uint32_t w) {
-  return __hiloint2double((static_cast<int>(w << 16) >> 3) & 0x8fffe000, 0);
+// High word of x * 2^-896 from the bits of the bf16 in the low or high half of w.
+__device__ __forceinline__ uint32_t bf16_lo_scaled_hi(uint32_t w) {
+  return static_cast<uint32_t>(static_cast<int>(w << 16) >> 3) & 0x8fffe000u;
 }
-__device__ __forceinline__ double bf16_hi_to_scaled(uint32_t w) {
-  return __hiloint2double((static_cast<int>(w) >> 3) & 0x8fffe000, 0);
+__device__ __forceinline__ uint32_t bf16_hi_scaled_hi(uint32_t w) {
+  return static_cast<uint32_t>(static_cast<int>(w) >> 3) & 0x8fffe000u;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kBtThreads) block_score_kernel(const __grid_constant__ BlockScoreArgs a) {
-  using C = BlockScoreCfg<D>;
+__global__ void __launch_bounds__(kBtThreads, 4) block_score_kernel(const __grid_constant__ BlockScoreArgs a) {
+  constexpr int LANES = D / 4, GROUPS = 32 / LANES, STEP = GROUPS * kBtBatch;
+  __shared__ float s_best[kBtWarps][kBtChunk];
+  const KvGeom& geo = a.geo;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / LANES, l = lane % LANES;
+  const int g = blockIdx.y % geo.G, b = blockIdx.y / geo.G;
   pdl_wait();  // inputs come from earlier work in the stream
   pdl_trigger();
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ double2 s_q[kBtHeads][D];  // (max(q, 0), min(q, 0)) * 2^800
-  const KvGeom& geo = a.geo;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = blockIdx.y % geo.G, b = blockIdx.y / geo.G;
   const int L = checked_seqlen(a.seqlens, b, a.cap);
   const int count = geo.bs_div.div(L + geo.bs - 1);
-  if (blockIdx.x == 0 && g == 0 && tid == 0) a.counts[b] = count;
-  if (blockIdx.x * kBtBlocks * kBtWarps >= count) return;
-  const int c0 = (blockIdx.x * kBtWarps + warp) * kBtBlocks;
-  unsigned char* rows = smem_raw + (size_t)warp * kBtBlocks * C::kRow;
+  if (blockIdx.x == 0 && g == 0 && threadIdx.x == 0) a.counts[b] = count;
+  const int c0 = (blockIdx.x * kBtWarps + warp) * a.chunk;
+  if (c0 >= count) return;
 
-  // ---- stage the bounds of this warp's blocks ----
+  // ---- where this warp's blocks are: one per lane ----
+  int blk = -1;
   const int c = c0 + lane;
-  long long at = -1;
-  if (c < count) {
+  if (lane < a.chunk && c < count) {
     const int tok = c * geo.bs, pi = geo.page_div.div(tok);
     const int page = a.block_table[(size_t)b * geo.max_pages + pi];
     if (page < 0 || page >= geo.num_pages) raise_error(SD_DEVERR_PAGE);
-    else at = ((long long)page * geo.blocks_per_page + geo.bs_div.div(tok - pi * geo.page_size)) * geo.G + g;
+    else blk = page * geo.blocks_per_page + geo.bs_div.div(tok - pi * geo.page_size);
   }
-  constexpr int kPieces = D / 4;  // 16-byte pieces of a row: [lo D][hi D]
-  constexpr int kRowsPerStep = 32 / kPieces;
-#pragma unroll 8
-  for (int i = 0; i < kBtBlocks; i += kRowsPerStep) {
-    const int r = i + lane / kPieces;
-    const long long src = __shfl_sync(0xffffffffu, at, r);
-    cp_async_16(rows + r * C::kRow + (lane % kPieces) * 16, a.bounds + max(src, 0LL) * 2 * D + (lane % kPieces) * 8,
-                src >= 0 ? 16 : 0);
-  }
-  cp_async_commit();
+  s_best[warp][lane] = -INFINITY;
+  __syncwarp();
 
-  double best = -INFINITY;
-  bool nan = false;
   for (int h0 = 0; h0 < a.qpk; h0 += kBtHeads) {
-    __syncthreads();
-    for (int i = tid; i < kBtHeads * D; i += kBtThreads) {
-      const int h = h0 + i / D;
-      const float x = h < a.qpk ? __bfloat162float(a.q[((size_t)b * a.H + g * a.qpk + h) * D + i % D]) : 0.f;
-      const double s = __longlong_as_double(0x71f0000000000000ll);  // 2^800
-      s_q[i / D][i % D] = x != x ? make_double2(x, x) : make_double2(fmaxf(x, 0.f) * s, fminf(x, 0.f) * s);
-    }
-    cp_async_wait<0>();
-    __syncthreads();
-    double acc[kBtHeads];
-#pragma unroll
-    for (int h = 0; h < kBtHeads; ++h) acc[h] = 0.0;
-    const uint4* lo = reinterpret_cast<const uint4*>(rows + lane * C::kRow);
-    const uint4* hi = lo + D / 8;
-#pragma unroll 2
-    for (int d = 0; d < D / 8; ++d) {
-      const uint4 x = lo[d], y = hi[d];
-      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const double kl = e ? bf16_hi_to_scaled(xw[w]) : bf16_lo_to_scaled(xw[w]);
-          const double kh = e ? bf16_hi_to_scaled(yw[w]) : bf16_lo_to_scaled(yw[w]);
-#pragma unroll
-          for (int h = 0; h < kBtHeads; ++h) {
-            const double2 qv = s_q[h][8 * d + 2 * w + e];
-            acc[h] = fma(qv.x, kh, fma(qv.y, kl, acc[h]));
-          }
-        }
-      }
-    }
+    // ---- four dims of four heads: value times 2^800, and which bound its sign picks ----
+    double q[kBtHeads][4];
+    uint32_t pick[kBtHeads][4];
 #pragma unroll
     for (int h = 0; h < kBtHeads; ++h) {
-      if (h0 + h >= a.qpk) continue;
-      nan |= acc[h] != acc[h];
-      best = fmax(best, acc[h]);
+      uint2 w = make_uint2(0u, 0u);
+      if (h0 + h < a.qpk) w = *reinterpret_cast<const uint2*>(a.q + ((size_t)b * a.H + g * a.qpk + h0 + h) * D + 4 * l);
+      const float2 x = bf2(w.x), y = bf2(w.y);
+      const float e[4] = {x.x, x.y, y.x, y.y};
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        q[h][d] = static_cast<double>(e[d]) * __longlong_as_double(0x71f0000000000000ll);  // 2^800
+        pick[h][d] = e[d] < 0.f ? 0x3210u : 0x7654u;
+      }
+    }
+    for (int i0 = 0; i0 < a.chunk && c0 + i0 < count; i0 += STEP) {
+      uint2 lo[kBtBatch], hi[kBtBatch];
+#pragma unroll
+      for (int i = 0; i < kBtBatch; ++i) {
+        const int at = __shfl_sync(0xffffffffu, blk, i0 + grp * kBtBatch + i);
+        lo[i] = hi[i] = make_uint2(0u, 0u);
+        if (at >= 0) {
+          const __nv_bfloat16* src = a.bounds + ((long long)at * geo.G + g) * (2 * D) + 4 * l;
+          lo[i] = *reinterpret_cast<const uint2*>(src);
+          hi[i] = *reinterpret_cast<const uint2*>(src + D);
+        }
+      }
+      double v[kBtBatch * kBtHeads];
+#pragma unroll
+      for (int i = 0; i < kBtBatch; ++i) {
+        const uint32_t kl[4] = {bf16_lo_scaled_hi(lo[i].x), bf16_hi_scaled_hi(lo[i].x), bf16_lo_scaled_hi(lo[i].y), bf16_hi_scaled_hi(lo[i].y)};
+        const uint32_t kh[4] = {bf16_lo_scaled_hi(hi[i].x), bf16_hi_scaled_hi(hi[i].x), bf16_lo_scaled_hi(hi[i].y), bf16_hi_scaled_hi(hi[i].y)};
+#pragma unroll
+        for (int h = 0; h < kBtHeads; ++h) {
+          double s = 0.0;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) s = fma(q[h][d], __hiloint2double(__byte_perm(kl[d], kh[d], pick[h][d]), 0), s);
+          v[i * kBtHeads + h] = s;
+        }
+      }
+      // sums over the LANES lanes: at each step a lane hands half of its
+      // values to its partner, so 16 values cost 16 exchanges, not 16 x 5
+      int n = kBtBatch * kBtHeads;
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) {
+        if (n > 1) {
+          const bool up = (l & o) != 0;
+#pragma unroll
+          for (int i = 0; i < kBtBatch * kBtHeads / 2; ++i) {
+            if (i < n / 2) {
+              const double mine = up ? v[i + n / 2] : v[i], other = up ? v[i] : v[i + n / 2];
+              v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+            }
+          }
+          n /= 2;
+        } else {
+          v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        }
+      }
+      // value of block (bits LANES/2, LANES/4 of l), head (the next two bits)
+      float f = static_cast<float>(v[0] * 7.9228162514264338e28);  // 2^96
+      const int head = ((l & (LANES / 8)) ? 2 : 0) + ((l & (LANES / 16)) ? 1 : 0);
+      if (f != f || h0 + head >= a.qpk) f = -INFINITY;  // a head that is not finite picks nothing
+      f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, LANES / 8));
+      f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, LANES / 16));
+      if ((l & (LANES / 4 - 1)) == 0) {
+        const int i = i0 + grp * kBtBatch + ((l & (LANES / 2)) ? 2 : 0) + ((l & (LANES / 4)) ? 1 : 0);
+        if (i < a.chunk) s_best[warp][i] = fmaxf(s_best[warp][i], f);
+      }
     }
   }
-  if (c >= count) return;
+  __syncwarp();
+  if (lane >= a.chunk || c >= count) return;
   int32_t key;
   if (c < a.n_first || c >= count - a.n_last) {
     key = INT32_MAX;  // always kept: above every score
   } else {
-    // fp32 bits as an integer of the same order; a NaN or a bad page counts as -inf
-    const float f = nan || at < 0 ? -INFINITY : static_cast<float>(best * 7.9228162514264338e28);  // 2^96
-    const int u = __float_as_int(f + 0.f);
+    // fp32 bits as an integer of the same order; a bad page counts as -inf
+    const int u = __float_as_int((blk < 0 ? -INFINITY : s_best[warp][lane]) + 0.f);
     key = u >= 0 ? u : (u ^ 0x7fffffff);
   }
   a.keys[((size_t)b * geo.G + g) * a.max_blocks + c] = key;
+}
+
+constexpr int kBsThreads = 256;
+constexpr int kBsPer = 16;                            // keys per thread
+constexpr int kBsMaxBlocks = kBsThreads * kBsPer;     // longest row
+constexpr int kBsBits = 11;
+constexpr int kBsBins = 1 << kBsBits;
+constexpr int kBsList = 256;                          // keys ranked directly
+
+// The min(n, count) largest keys of each row, ties to the lower index, written
+// ascending and padded with -1.
+__global__ void __launch_bounds__(kBsThreads) block_select_kernel(const int32_t* __restrict__ keys,
+                                                                 const int32_t* __restrict__ counts, int G, int max_blocks,
+                                                                 int n, int32_t* __restrict__ indices) {
+  constexpr int kWarps = kBsThreads / 32;
+  __shared__ uint32_t s_hist[kBsBins];
+  __shared__ uint32_t s_min[kWarps], s_max[kWarps];
+  __shared__ int s_sum[kWarps], s_forced[kWarps];
+  __shared__ uint32_t s_list[kBsList];
+  __shared__ int s_n, s_digit, s_above;
+  __shared__ uint32_t s_key;
+  __shared__ int s_take;
+  __shared__ int s_cnt[kBsPer * kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.x;
+  for (int i = tid; i < kBsBins; i += kBsThreads) s_hist[i] = 0u;
+  if (tid == 0) s_n = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int count = counts[row / G];
+  int32_t* out = indices + (size_t)row * n;
+  if (count <= n) {  // everything is kept
+    for (int i = tid; i < n; i += kBsThreads) out[i] = i < count ? i : -1;
+    return;
+  }
+  const int per = ceil_div(count, kBsThreads);
+  uint32_t k[kBsPer];  // as unsigned integers of the same order; 0 behind the row
+  uint32_t mn = ~0u, mx = 0u;
+  int forced = 0;
+#pragma unroll
+  for (int i = 0; i < kBsPer; ++i) {
+    k[i] = 0u;
+    const int c = i * kBsThreads + tid;
+    if (i < per && c < count) k[i] = static_cast<uint32_t>(keys[(size_t)row * max_blocks + c]) ^ 0x80000000u;
+  }
+#pragma unroll
+  for (int i = 0; i < kBsPer; ++i) {
+    const bool live = i * kBsThreads + tid < count;
+    forced += live && k[i] == ~0u;
+    if (live && k[i] != ~0u) mn = min(mn, k[i]), mx = max(mx, k[i]);
+  }
+  mn = __reduce_min_sync(0xffffffffu, mn);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  forced = __reduce_add_sync(0xffffffffu, forced);
+  if (lane == 0) s_min[warp] = mn, s_max[warp] = mx, s_forced[warp] = forced;
+  __syncthreads();
+  forced = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) mn = min(mn, s_min[w]), mx = max(mx, s_max[w]), forced += s_forced[w];
+  // the keys that are not forced, of which `want` >= 0 are taken: all lie in
+  // [mn, mx]. T: the smallest key taken, take: how many equal to it
+  int want = n - forced;
+  uint32_t T = ~0u;
+  int take = 0;
+  if (want > 0) {
+    int top = 32 - __clz(static_cast<int>(mn ^ mx));  // bits [top, 32) are the same in all
+    uint32_t prefix = top == 32 ? 0u : mx >> top;     // of the keys still in question
+    while (true) {
+      const int shift = max(0, top - kBsBits);
+      const uint32_t mask = (1u << (top - shift)) - 1u;  // top - shift <= 11
+      auto in = [&](uint32_t x) { return x != ~0u && x >= mn && (top == 32 ? 0u : x >> top) == prefix; };
+#pragma unroll
+      for (int i = 0; i < kBsPer; ++i)
+        if (i * kBsThreads + tid < count && in(k[i])) atomicAdd(&s_hist[(k[i] >> shift) & mask], 1u);
+      __syncthreads();
+      // from the highest digit down: thread t holds bins [t * 8, t * 8 + 8)
+      constexpr int kBinsPer = kBsBins / kBsThreads;
+      uint32_t h[kBinsPer];
+      int own = 0;
+#pragma unroll
+      for (int j = 0; j < kBinsPer; ++j) h[j] = s_hist[tid * kBinsPer + j], own += h[j];
+      int incl = own;  // this thread's bins and all higher ones of the warp
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_down_sync(0xffffffffu, incl, o);
+        if (lane + o < 32) incl += x;
+      }
+      if (lane == 0) s_sum[warp] = incl;
+      __syncthreads();
+      int above = incl - own;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) above += w > warp ? s_sum[w] : 0;
+      if (above < want && above + own >= want) {
+#pragma unroll
+        for (int j = kBinsPer - 1; j >= 0; --j) {
+          if (above < want && above + static_cast<int>(h[j]) >= want) s_digit = tid * kBinsPer + j, s_above = above;
+          above += h[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBinsPer; ++j) s_hist[tid * kBinsPer + j] = 0u;  // for the next round
+      __syncthreads();
+      want -= s_above;  // still to take from this digit
+      prefix = (prefix << (top - shift)) | static_cast<uint32_t>(s_digit);
+      top = shift;
+      // gather the digit's keys; too many of them overrun the list, not its end
+#pragma unroll
+      for (int i = 0; i < kBsPer; ++i) {
+        if (i * kBsThreads + tid < count && in(k[i])) {
+          const int at = atomicAdd(&s_n, 1);
+          if (at < kBsList) s_list[at] = k[i];
+        }
+      }
+      __syncthreads();
+      const int m = s_n;
+      if (m <= kBsList) {
+        if (tid < m) {
+          const uint32_t x = s_list[tid];
+          int more = 0, same = 0;
+          for (int j = 0; j < m; ++j) more += s_list[j] > x, same += s_list[j] == x;
+          if (more < want && more + same >= want) s_key = x, s_take = want - more;  // equal keys write the same
+        }
+        __syncthreads();
+        T = s_key, take = s_take;
+        break;
+      }
+      if (top == 0) {  // all equal
+        T = prefix, take = want;
+        break;
+      }
+      __syncthreads();
+      if (tid == 0) s_n = 0;
+    }
+  }
+  // ---- ordered output: key > T, and the first `take` keys equal to T ----
+#pragma unroll
+  for (int i = 0; i < kBsPer; ++i) {
+    if (i >= per) break;
+    const bool live = i * kBsThreads + tid < count;
+    const unsigned int gt = __ballot_sync(0xffffffffu, live && (k[i] > T || (k[i] == ~0u))), eq = __ballot_sync(0xffffffffu, live && k[i] == T && k[i] != ~0u);
+    if (lane == 0) s_cnt[i * kWarps + warp] = __popc(gt) | (__popc(eq) << 16);
+  }
+  __syncthreads();
+  if (warp == 0) {  // exclusive prefix over (i, warp) in index order
+    const int m = per * kWarps;
+    int c[kBsPer * kWarps / 32], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kBsPer * kWarps / 32; ++j) {
+      const int at = lane * (kBsPer * kWarps / 32) + j;
+      c[j] = at < m ? s_cnt[at] : 0;
+      sum += c[j];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    int at = incl - sum;
+#pragma unroll
+    for (int j = 0; j < kBsPer * kWarps / 32; ++j) {
+      s_cnt[lane * (kBsPer * kWarps / 32) + j] = at;
+      at += c[j];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kBsPer; ++i) {
+    if (i >= per) break;
+    const int c = i * kBsThreads + tid;
+    const bool live = c < count;
+    const bool is_gt = live && (k[i] > T || k[i] == ~0u), is_eq = live && k[i] == T && k[i] != ~0u;
+    const unsigned int gt = __ballot_sync(0xffffffffu, is_gt), eq = __ballot_sync(0xffffffffu, is_eq);
+    const unsigned int lower = (1u << lane) - 1u;
+    const int before = s_cnt[i * kWarps + warp];
+    const int g0 = (before & 0xffff) + __popc(gt & lower), e0 = (before >> 16) + __popc(eq & lower);
+    if (is_gt || (is_eq && e0 < take)) out[g0 + min(e0, take)] = c;
+  }
 }
 
 }  // namespace sd

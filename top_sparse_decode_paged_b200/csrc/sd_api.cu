@@ -1105,7 +1105,7 @@ sd_status check_block_topk_args(const uint16_t* q, const sd_kv_cache& kv, const 
   if (!kv.k_bounds || B < 0 || H <= 0 || H % pd.kv_heads != 0 || max_seqlen < 0 || n_select <= 0 || n_first < 0 ||
       n_last < 0 || (long long)n_first + n_last > n_select)
     return SD_ERR_INVALID_ARG;
-  if (B > 0 && (!q || !bt || !seqlens || !indices)) return SD_ERR_INVALID_ARG;
+  if (B > 0 && (!q || !bt || !seqlens || !indices || !aligned(q, 8))) return SD_ERR_INVALID_ARG;
   if (n_select > kMaxK || H / pd.kv_heads > 128 || (long long)B * pd.kv_heads > 65535 ||
       (max_seqlen + (long long)kv.block_tokens - 1) / kv.block_tokens > kMaxSeqlen)
     return SD_ERR_UNSUPPORTED;
@@ -1113,12 +1113,13 @@ sd_status check_block_topk_args(const uint16_t* q, const sd_kv_cache& kv, const 
 }
 
 template <int D>
-sd_status launch_block_score(const sd::BlockScoreArgs& a, cudaStream_t st) {
-  constexpr size_t smem = sd::BlockScoreCfg<D>::kSmem;
-  const sd_status s = set_smem_limit(reinterpret_cast<const void*>(sd::block_score_kernel<D>), smem);
-  if (s != SD_OK) return s;
-  const dim3 grid(std::max(1, sd::ceil_div(a.max_blocks, sd::kBtBlocks * sd::kBtWarps)), a.B * a.geo.G);
-  return launch_k(sd::block_score_kernel<D>, grid, dim3(sd::kBtThreads), smem, st, a);
+sd_status launch_block_score(sd::BlockScoreArgs& a, cudaStream_t st) {
+  // blocks per warp: as many as leave two warps per scheduler
+  a.chunk = sd::kBtChunk;
+  const long long blocks = (long long)a.B * a.geo.G * a.max_blocks;
+  while (a.chunk > 8 && blocks < 148ll * 8 * a.chunk) a.chunk /= 2;
+  const dim3 grid(std::max(1, sd::ceil_div(a.max_blocks, a.chunk * sd::kBtWarps)), a.B * a.geo.G);
+  return launch_k(sd::block_score_kernel<D>, grid, dim3(sd::kBtThreads), 0, st, a);
 }
 
 sd_status launch_block_topk(const uint16_t* q, const sd_kv_cache& kv, const int32_t* bt, const int32_t* seqlens,
@@ -1145,7 +1146,14 @@ sd_status launch_block_topk(const uint16_t* q, const sd_kv_cache& kv, const int3
   const sd_status s = kv.D == 64 ? launch_block_score<64>(a, st) : launch_block_score<128>(a, st);
   stage_mark(kStageIndexer, 1, st);
   if (s != SD_OK) return s;
-  return launch_topk(a.keys, a.counts, indices, B, G, max_blocks, max_blocks, n_select, sd::RowMap{}, nullptr, st);
+  if (max_blocks > sd::kBsMaxBlocks)
+    return launch_topk(a.keys, a.counts, indices, B, G, max_blocks, max_blocks, n_select, sd::RowMap{}, nullptr, st);
+  stage_mark(kStageTopk, 0, st);
+  const sd_status s2 = launch_k(sd::block_select_kernel, dim3(B * G), dim3(sd::kBsThreads), 0, st,
+                                static_cast<const int32_t*>(a.keys), static_cast<const int32_t*>(a.counts), G,
+                                std::max(max_blocks, 1), n_select, indices);
+  stage_mark(kStageTopk, 1, st);
+  return s2;
 }
 
 }  // namespace
