@@ -423,13 +423,19 @@ SD_KV_E4M3 = 2
 _KV_TYPES = {torch.bfloat16: SD_KV_BF16, torch.int8: SD_KV_INT8, torch.float8_e4m3fn: SD_KV_E4M3}
 
 
-def _need(t: torch.Tensor, name: str, dtype, shape, device) -> int:
-    """The data pointer of a contiguous tensor of that type, shape and device."""
+def _need(t: torch.Tensor, name: str, dtype, shape, device: int) -> int:
+    """The data pointer of a contiguous tensor of that type and shape on GPU ``device``."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype or tuple(t.shape) != shape:
         raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous and on cuda:{device}")
+
+
+# The handle of a device's current stream. The public call builds a Stream
+# object (2 us on the decode path), this one returns the number alone.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 class KvCache:
@@ -450,35 +456,43 @@ class KvCache:
         self.device = k_pages.device
         if self.device.type != "cuda":
             raise ValueError("tensors passed to the library must be on the GPU")
+        dev = self._dev = k_pages.get_device()
         self.num_pages, self.page_size, self.G, self.D, self.block_tokens = N, P, G, D, bs
         self.kv_type = _KV_TYPES[k_pages.dtype]
-        kp = _need(k_pages, "k_pages", k_pages.dtype, (N, P, G, D), self.device)
-        vp = _need(v_pages, "v_pages", k_pages.dtype, (N, P, G, D), self.device)
+        kp = _need(k_pages, "k_pages", k_pages.dtype, (N, P, G, D), dev)
+        vp = _need(v_pages, "v_pages", k_pages.dtype, (N, P, G, D), dev)
         ks = vs = kb = None
         if self.kv_type != SD_KV_BF16:
             if k_scales is None or v_scales is None:
                 raise ValueError("8-bit pools need k_scales and v_scales")
-            ks = _need(k_scales, "k_scales", torch.float32, (N, P // bs, G), self.device)
-            vs = _need(v_scales, "v_scales", torch.float32, (N, P // bs, G), self.device)
+            ks = _need(k_scales, "k_scales", torch.float32, (N, P // bs, G), dev)
+            vs = _need(v_scales, "v_scales", torch.float32, (N, P // bs, G), dev)
         if k_bounds is not None:
-            kb = _need(k_bounds, "k_bounds", torch.bfloat16, (N, P // bs, G, 2, D), self.device)
+            kb = _need(k_bounds, "k_bounds", torch.bfloat16, (N, P // bs, G, 2, D), dev)
         self.k_pages, self.v_pages, self.k_scales, self.v_scales, self.k_bounds = k_pages, v_pages, k_scales, v_scales, k_bounds
         self._kv = KvDesc(kp, vp, ks, vs, kb, self.kv_type, bs, D)
+        self._descs = {}  # PagedDesc by block-table width
 
     def _paged(self, block_table, B: int):
-        if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
-                block_table.device != self.device or not block_table.is_contiguous():
-            raise ValueError(f"block_table must be contiguous int32 [{B}, pages] on {self.device}")
-        return block_table.data_ptr(), PagedDesc(self.num_pages, self.page_size, block_table.shape[1], self.G)
+        shape = block_table.shape
+        if len(shape) != 2 or shape[0] != B or block_table.dtype is not torch.int32:
+            raise ValueError(f"block_table must be int32 [{B}, pages]")
+        width = shape[1]
+        pd = self._descs.get(width)
+        if pd is None:
+            pd = self._descs[width] = PagedDesc(self.num_pages, self.page_size, width, self.G)
+        return _need(block_table, "block_table", torch.int32, shape, self._dev), pd
 
     def _call(self, stream, fn, *args):
-        """Enqueues on ``stream`` or the cache's device's current one, with that device current."""
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        if torch.cuda.current_device() == self.device.index:
-            _check(fn(*args, s.cuda_stream))
+        """Enqueues on ``stream`` or the device's current one, with the cache's device current."""
+        st = _raw_stream(self._dev) if stream is None else stream.cuda_stream
+        if torch.cuda.current_device() == self._dev:
+            status = fn(*args, st)
         else:
-            with torch.cuda.device(self.device):
-                _check(fn(*args, s.cuda_stream))
+            with torch.cuda.device(self._dev):
+                status = fn(*args, st)
+        if status != 0:
+            _check(status)
 
     def _empty(self, shape, dtype, stream):
         """A new tensor whose memory belongs to the stream the call runs on."""
@@ -506,12 +520,12 @@ def alloc_kv_cache(num_pages: int, page_size: int, G: int, D: int, dtype=torch.i
 def _rows(t, name: str, T: int, heads: int, cache: KvCache):
     """Pointer and row stride of token rows [T, heads, D] whose heads are dense."""
     D = cache.D
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, heads, D) or t.device != cache.device:
+    if t.dtype is not torch.bfloat16 or t.shape != (T, heads, D) or t.get_device() != cache._dev:
         raise ValueError(f"{name}: expected bf16 {(T, heads, D)} on {cache.device}, got {t.dtype} {tuple(t.shape)}")
-    st = t.stride()
-    if T > 0 and (st[2] != 1 or (heads > 1 and st[1] != D)):
+    row, head, one = t.stride()
+    if T > 0 and (one != 1 or (heads > 1 and head != D)):
         raise ValueError(f"{name}: the heads of a token must be dense")
-    return t.data_ptr(), st[0] if T > 1 else heads * D
+    return t.data_ptr(), row if T > 1 else heads * D
 
 
 def sd_kv_store(q, k, v, cache: KvCache, block_table, seqlens, tok_start, inv_freq, q_weight=None, k_weight=None,
@@ -522,7 +536,7 @@ def sd_kv_store(q, k, v, cache: KvCache, block_table, seqlens, tok_start, inv_fr
     rows are ``tok_start[b]:tok_start[b + 1]``. ``inv_freq`` is fp32
     [rot_dim / 2] or None. Returns ``q_out`` [T, H, D] bf16 (None without q)."""
     B, T = seqlens.shape[0], k.shape[0]
-    G, D, dev = cache.G, cache.D, cache.device
+    G, D, dev = cache.G, cache.D, cache._dev
     kp, ks = _rows(k, "k", T, G, cache)
     vp, vs = _rows(v, "v", T, G, cache)
     qp, qs, H, qo = None, 0, 0, None
@@ -549,7 +563,7 @@ def sd_kv_load(cache: KvCache, block_table, seqlens, tok_start, n_tokens: int, k
     """The tokens that ``sd_kv_store`` with the same arguments stores, read
     back as bf16. Returns ``(k_out, v_out)`` [n_tokens, G, D]; rows behind
     ``tok_start[B]`` are left as they are."""
-    B, dev, shape = seqlens.shape[0], cache.device, (n_tokens, cache.G, cache.D)
+    B, dev, shape = seqlens.shape[0], cache._dev, (n_tokens, cache.G, cache.D)
     if k_out is None:
         k_out = cache._empty(shape, torch.bfloat16, stream)
     if v_out is None:
@@ -583,9 +597,9 @@ def alloc_block_step_workspace(B: int, G: int, H: int, D: int, max_seqlen: int, 
 def _workspace(workspace, nbytes: int, cache: KvCache, stream):
     if workspace is None:
         workspace = cache._empty((max(nbytes, 1),), torch.uint8, stream)
-    if workspace.device != cache.device or not workspace.is_contiguous():
+    if workspace.get_device() != cache._dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {cache.device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def sd_kv_attn(q, cache: KvCache, block_table, seqlens, scale: float, indices=None, index_block: int = 1, out=None,
@@ -595,7 +609,7 @@ def sd_kv_attn(q, cache: KvCache, block_table, seqlens, scale: float, indices=No
     lists (1: tokens). Returns ``out`` [B, H, D] bf16."""
     lib = load_library()
     B, H = q.shape[0], q.shape[1]
-    G, D, dev = cache.G, cache.D, cache.device
+    G, D, dev = cache.G, cache.D, cache._dev
     if out is None:
         out = cache._empty((B, H, D), torch.bfloat16, stream)
     n, ip = 0, None
@@ -619,7 +633,7 @@ def sd_block_topk(q, cache: KvCache, block_table, seqlens, n_select: int, max_se
     Returns ``indices`` [B, G, n_select] int32, ascending, -1 padded."""
     lib = load_library()
     B, H = q.shape[0], q.shape[1]
-    G, D, dev = cache.G, cache.D, cache.device
+    G, D, dev = cache.G, cache.D, cache._dev
     if indices is None:
         indices = cache._empty((B, G, n_select), torch.int32, stream)
     ws, ws_bytes = _workspace(workspace, 0 if workspace is not None else
@@ -637,7 +651,7 @@ def sd_kv_block_step(q, cache: KvCache, block_table, seqlens, n_select: int, max
     Returns (indices [B, G, n_select] int32, out [B, H, D] bf16)."""
     lib = load_library()
     B, H = q.shape[0], q.shape[1]
-    G, D, dev = cache.G, cache.D, cache.device
+    G, D, dev = cache.G, cache.D, cache._dev
     if indices is None:
         indices = cache._empty((B, G, n_select), torch.int32, stream)
     if out is None:

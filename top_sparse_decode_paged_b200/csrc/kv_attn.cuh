@@ -50,7 +50,6 @@ constexpr int kKaWarps = kKaThreads / 32;
 constexpr int kKaTile = 32;      // tokens per tile: one lookup per lane
 constexpr int kKaStep = 16;      // tokens per stage
 constexpr int kKaRanges = 296;   // CTAs of a column group in one wave: two per SM
-constexpr int kKaMinTiles = 1;   // fewest tiles a range gets (shorter lists use fewer ranges)
 constexpr float kKaSlack = 8.f;  // log2: how far a weight may pass the running reference
 
 struct KvAttnArgs {
@@ -97,10 +96,21 @@ __device__ __forceinline__ int kv_attn_len(const KvAttnArgs& a, int b) {
 __device__ __forceinline__ int kv_attn_tiles(const KvAttnArgs& a, int b) {
   return ceil_div(kv_attn_len(a, b), kKaTile * a.spw);
 }
-// How many ranges the list of `total` tiles is cut into.
-__device__ __forceinline__ int kv_attn_ranges(const KvAttnArgs& a, long long total) {
-  return static_cast<int>(max(1LL, min((long long)a.ranges, total / kKaMinTiles)));
-}
+// The list of `total` tiles cut into n ranges: the first `extra` have q + 1
+// tiles, the others q.
+struct KvAttnCut {
+  int n, q, extra;
+  __device__ __forceinline__ KvAttnCut(const KvAttnArgs& a, int total) {
+    n = max(1, min(a.ranges, total));
+    q = total / n;
+    extra = total - q * n;
+  }
+  __device__ __forceinline__ int start(int i) const { return i * q + min(i, extra); }
+  __device__ __forceinline__ int range_of(int t) const {
+    const int big = extra * (q + 1);
+    return t < big ? t / (q + 1) : extra + (t - big) / q;
+  }
+};
 
 __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -191,28 +201,32 @@ __device__ __forceinline__ uint32_t q_part(const float* x, int p) {
   return w;
 }
 
-// Tiles of all requests, by one warp.
-__device__ __forceinline__ long long kv_attn_total(const KvAttnArgs& a) {
-  long long n = 0;
-  for (int b = threadIdx.x & 31; b < a.B; b += 32) n += kv_attn_tiles(a, b);
+__device__ __forceinline__ int warp_inclusive_sum(int x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
 }
 
-// The request that holds tile t < total of the list, and its first tile, by
-// one warp.
-__device__ __forceinline__ int kv_attn_find(const KvAttnArgs& a, long long t, long long* first) {
+// Tiles of requests [0, end), by one warp.
+__device__ __forceinline__ int kv_attn_sum(const KvAttnArgs& a, int end) {
+  int n = 0;
+  for (int b = threadIdx.x & 31; b < end; b += 32) n += kv_attn_tiles(a, b);
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// The request that holds tile t of the list, and its first tile, by one
+// warp; cnt and incl are the first 32 requests' tiles and their inclusive sums.
+__device__ __forceinline__ int kv_attn_find(const KvAttnArgs& a, int t, int cnt, int incl, int* first) {
   const int lane = threadIdx.x & 31;
-  long long before = 0;
+  int before = 0;
   for (int base = 0;; base += 32) {
-    const int b = base + lane;
-    const int cnt = b < a.B ? kv_attn_tiles(a, b) : 0;
-    int incl = cnt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+    if (base > 0) {
+      cnt = base + lane < a.B ? kv_attn_tiles(a, base + lane) : 0;
+      incl = warp_inclusive_sum(cnt);
     }
     const unsigned int past = __ballot_sync(0xffffffffu, before + incl > t);
     if (past != 0 || base + 32 >= a.B) {
@@ -239,13 +253,15 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
 
   // ---- this CTA's range of the tile list, and the request it starts in
   // (every warp finds them for itself: no barrier) ----
-  const long long total = kv_attn_total(a);
-  const int nr = kv_attn_ranges(a, total);
-  if (blockIdx.x >= nr || total == 0) return;
-  const long long t_begin = blockIdx.x * total / nr, t_end = (blockIdx.x + 1) * total / nr;
-  long long first;
-  const int b_begin = kv_attn_find(a, t_begin, &first);
-  const int tile_begin = static_cast<int>(t_begin - first);
+  const int cnt = lane < a.B ? kv_attn_tiles(a, lane) : 0, incl = warp_inclusive_sum(cnt);
+  const int total = a.B <= 32 ? __shfl_sync(0xffffffffu, incl, 31) : kv_attn_sum(a, a.B);
+  const KvAttnCut cut(a, total);
+  const int range = blockIdx.x;
+  if (range >= cut.n || total == 0) return;
+  const int t_begin = cut.start(range), t_end = cut.start(range + 1);
+  int first;
+  const int b_begin = kv_attn_find(a, t_begin, cnt, incl, &first);
+  const int tile_begin = t_begin - first;
 
   // ---- this warp's column ----
   const int col = a.cols >= kKaWarps ? blockIdx.y * kKaWarps + warp : warp % a.cols;
@@ -255,7 +271,7 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
   const int g = col / hblocks, h0 = g * a.qpk + (col % hblocks) * HPW;
   const int nh = min(HPW, (g + 1) * a.qpk - h0);
   unsigned char* ring = smem_raw + (size_t)warp * C::kStages * C::kStage;
-  const int my = 2 * static_cast<int>(t_end - t_begin);  // stages: two per tile
+  const int my = 2 * (t_end - t_begin);  // stages: two per tile
 
   // ---- the copy side, one row per lane and tile, three steps ahead of each
   // other, so that a list entry, its page and its row are never waited for
@@ -428,7 +444,7 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
     }
   };
   auto flush = [&]() {
-    const size_t slot = ((size_t)blockIdx.x + cb) * a.spw + sub;
+    const size_t slot = ((size_t)range + cb) * a.spw + sub;
 #pragma unroll
     for (int i = 0; i < C::kHL; ++i) {
       float s = l[i];
@@ -613,91 +629,93 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
 }
 
 // Merges the partials of one (request, query head): with M = max M_i,
-// o = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i. One CTA each; a group of
-// D / 4 lanes takes every GROUPS-th partial, a batch of them in flight
-// together with their (M, l), and keeps a running maximum: one trip to L2
-// for up to kKaBatch * GROUPS partials. The list is walked before the wait for the
-// attention.
-constexpr int kKaCombineThreads = 256;
-constexpr int kKaBatch = 4;
-
-template <int D>
-__global__ void __launch_bounds__(kKaCombineThreads) kv_attn_combine_kernel(const __grid_constant__ KvAttnArgs a) {
-  constexpr int LANES = D / 4, GROUPS = kKaCombineThreads / LANES;
-  __shared__ float2 s_ml[GROUPS];
-  __shared__ float4 s_o[GROUPS][LANES];
-  const int tid = threadIdx.x;
-  const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
+// o = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i. A CTA takes 4 LANES dims
+// of it; a group of LANES lanes takes every GROUPS-th partial, BATCH of them
+// in flight together with their (M, l): one trip to L2 for up to BATCH *
+// GROUPS partials. Few rows have many partials each and take narrow groups
+// (LANES 8, 256 threads), many rows have few and take whole rows (LANES D / 4, 128
+// threads). The list is walked before the wait for the attention.
+template <int D, int LANES, int THREADS, int BATCH>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_attn_combine_kernel(const __grid_constant__ KvAttnArgs a) {
+  constexpr int GROUPS = THREADS / LANES, SLICES = D / (4 * LANES), WARPS = THREADS / 32;
+  __shared__ float2 s_ml[WARPS];
+  __shared__ float4 s_o[WARPS][LANES];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bh = blockIdx.x / SLICES, slice = blockIdx.x - bh * SLICES;
+  const int b = bh / a.H, h = bh - b * a.H;
   // the caller's lengths: no kernel of this call writes them, and this kernel
   // starts only after the attention has passed its own wait
-  const long long total = kv_attn_total(a);
-  long long first = 0;
-  for (int i = tid & 31; i < b; i += 32) first += kv_attn_tiles(a, i);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-  const int tiles = kv_attn_tiles(a, b);
-  const size_t bh = (size_t)b * a.H + h;
-  const int grp = tid / LANES, ln = tid % LANES;
+  int total, first, tiles;
+  if (a.B <= 32) {
+    const int cnt = lane < a.B ? kv_attn_tiles(a, lane) : 0, incl = warp_inclusive_sum(cnt);
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    first = __shfl_sync(0xffffffffu, incl - cnt, b);
+    tiles = __shfl_sync(0xffffffffu, cnt, b);
+  } else {
+    total = kv_attn_sum(a, a.B);
+    first = kv_attn_sum(a, b);
+    tiles = kv_attn_tiles(a, b);
+  }
   int parts = 0;
   size_t slot0 = 0;
   if (tiles > 0) {
-    const int nr = kv_attn_ranges(a, total);
-    const long long r0 = ((first + 1) * nr - 1) / total, r1 = ((first + tiles) * nr - 1) / total;
-    parts = static_cast<int>(r1 - r0 + 1) * a.spw;
+    const KvAttnCut cut(a, total);
+    const int r0 = cut.range_of(first), r1 = cut.range_of(first + tiles - 1);
+    parts = (r1 - r0 + 1) * a.spw;
     slot0 = (size_t)(r0 + b) * a.spw;
   }
+  const int grp = tid / LANES, ln = tid % LANES;
+  const float2* ml_at = a.part_ml + (slot0 + grp) * a.H + h;
+  const float* o_at = a.part_o + ((slot0 + grp) * a.H + h) * D + slice * (4 * LANES) + 4 * ln;
+  const size_t hop = (size_t)GROUPS * a.H;
   pdl_wait();
   pdl_trigger();
   float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = grp; i0 < parts; i0 += GROUPS * kKaBatch) {
-    float2 ml[kKaBatch];
-    float4 x[kKaBatch];
+  // adds a partial to (M, l, acc); a sum of 0 means that it has no token
+  auto add = [&](float m2, float l2, const float4& x) {
+    const float m = fmaxf(M, m2);
+    const float f1 = l == 0.f ? 0.f : exp2f(M - m), f2 = l2 == 0.f ? 0.f : exp2f(m2 - m);
+    M = m;
+    l = f1 * l + f2 * l2;
+    acc.x = f1 * acc.x + f2 * x.x, acc.y = f1 * acc.y + f2 * x.y;
+    acc.z = f1 * acc.z + f2 * x.z, acc.w = f1 * acc.w + f2 * x.w;
+  };
+  for (int i0 = grp; i0 < parts; i0 += GROUPS * BATCH) {
+    float2 ml[BATCH];
+    float4 x[BATCH];
 #pragma unroll
-    for (int j = 0; j < kKaBatch; ++j) {
-      const int i = i0 + j * GROUPS;
+    for (int j = 0; j < BATCH; ++j) {
       ml[j] = make_float2(-INFINITY, 0.f);
       x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < parts) {
-        const size_t at = (slot0 + i) * a.H + h;
-        ml[j] = a.part_ml[at];
-        x[j] = *reinterpret_cast<const float4*>(a.part_o + at * D + 4 * ln);
+      if (i0 + j * GROUPS < parts) {
+        ml[j] = *ml_at;
+        x[j] = *reinterpret_cast<const float4*>(o_at);
       }
+      ml_at += hop;
+      o_at += hop * D;
     }
-    float m = M;
 #pragma unroll
-    for (int j = 0; j < kKaBatch; ++j) m = fmaxf(m, ml[j].x);
-    const float back = M == -INFINITY ? 0.f : exp2f(M - m);
-    M = m;
-    l *= back;
-    acc.x *= back, acc.y *= back, acc.z *= back, acc.w *= back;
-#pragma unroll
-    for (int j = 0; j < kKaBatch; ++j) {
-      const float f = ml[j].y == 0.f ? 0.f : exp2f(ml[j].x - m);  // sum 0: no token there
-      l += f * ml[j].y;
-      acc.x += f * x[j].x, acc.y += f * x[j].y, acc.z += f * x[j].z, acc.w += f * x[j].w;
-    }
+    for (int j = 0; j < BATCH; ++j)
+      if (i0 + j * GROUPS < parts) add(ml[j].x, ml[j].y, x[j]);
   }
-  s_o[grp][ln] = acc;
-  if (ln == 0) s_ml[grp] = make_float2(M, l);
+#pragma unroll
+  for (int o = LANES; o < 32; o <<= 1) {  // the groups of a warp
+    const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+    const float4 x = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
+                                 __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
+    add(m2, l2, x);
+  }
+  if (lane < LANES) s_o[warp][lane] = acc;
+  if (lane == 0) s_ml[warp] = make_float2(M, l);
   __syncthreads();
   if (tid >= LANES) return;
 #pragma unroll
-  for (int i = 0; i < GROUPS; ++i) M = fmaxf(M, s_ml[i].x);
-  l = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < GROUPS; ++i) {
-    const float2 ml = s_ml[i];
-    const float4 x = s_o[i][ln];
-    const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
-    l += f * ml.y;
-    acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
-  }
+  for (int w = 1; w < WARPS; ++w) add(s_ml[w].x, s_ml[w].y, s_o[w][tid]);
   const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: nothing was attended
-  *reinterpret_cast<uint2*>(a.out + bh * D + 4 * ln) =
+  *reinterpret_cast<uint2*>(a.out + (size_t)bh * D + slice * (4 * LANES) + 4 * tid) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (a.lse != nullptr && ln == 0) a.lse[bh] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994530942f;
+  if (a.lse != nullptr && slice == 0 && tid == 0) a.lse[bh] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994530942f;
 }
 
 }  // namespace sd

@@ -1026,7 +1026,9 @@ sd_status check_kv_attn_args(const uint16_t* q, const sd_kv_cache& kv, const int
   if (B > 0 && (!q || !bt || !seqlens || !out || !aligned(q, 16) || !aligned(out, 8))) return SD_ERR_INVALID_ARG;
   // rows are addressed in 16-byte units held in 32 bits: pools up to 64 GiB
   if ((unsigned long long)pd.num_pages * pd.page_size * pd.kv_heads * kv.D >= (1ull << 36) - 16) return SD_ERR_UNSUPPORTED;
-  if (kv.kv_type == SD_KV_BF16 || H / pd.kv_heads > 128 || (long long)B * H >= (1ll << 31)) return SD_ERR_UNSUPPORTED;
+  if (kv.kv_type == SD_KV_BF16 || H / pd.kv_heads > 128 || (long long)B * H >= (1ll << 29) ||
+      (long long)B * pd.max_pages_per_req * pd.page_size >= (1ll << 36))  // tiles are counted in 32 bits
+    return SD_ERR_UNSUPPORTED;
   return SD_OK;
 }
 
@@ -1037,6 +1039,16 @@ sd_status launch_kv_attn_t(const sd::KvAttnArgs& a, cudaStream_t st) {
   const sd_status s = set_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (s != SD_OK) return s;
   return launch_k(kern, dim3(a.ranges, a.col_groups), dim3(sd::kKaThreads), smem, st, a);
+}
+
+template <int D>
+sd_status launch_kv_combine(const sd::KvAttnArgs& a, cudaStream_t st) {
+  // narrow groups while one wave holds their CTAs (four per SM)
+  constexpr int kSlices = D / 32;
+  const int rows = a.B * a.H;
+  if ((long long)rows * kSlices <= 4 * 148)
+    return launch_k(sd::kv_attn_combine_kernel<D, 8, 256, 4>, dim3(rows * kSlices), dim3(256), 0, st, a);
+  return launch_k(sd::kv_attn_combine_kernel<D, D / 4, 128, 8>, dim3(rows), dim3(128), 0, st, a);
 }
 
 sd_status launch_kv_attn(const uint16_t* q, const sd_kv_cache& kv, const int32_t* bt, const int32_t* seqlens,
@@ -1086,8 +1098,7 @@ sd_status launch_kv_attn(const uint16_t* q, const sd_kv_cache& kv, const int32_t
   stage_mark(kStageAttn, 1, st);
   if (s != SD_OK) return s;
   stage_mark(kStageCombine, 0, st);
-  s = launch_k(kv.D == 64 ? sd::kv_attn_combine_kernel<64> : sd::kv_attn_combine_kernel<128>, dim3(B * H),
-               dim3(sd::kKaCombineThreads), 0, st, a);
+  s = kv.D == 64 ? launch_kv_combine<64>(a, st) : launch_kv_combine<128>(a, st);
   stage_mark(kStageCombine, 1, st);
   return s;
 }
