@@ -6,32 +6,38 @@
 // `index_block` tokens per (request, KV head) (1: the tokens an indexer
 // selects).
 //
-// Mathematics. q . k8 runs on the 8-bit matrix instructions with K's codes
-// as they lie in the cache: q is cut into parts of the cache's own type whose
-// weighted sum is q. int8: q * S rounded to a 23-bit integer (S a power of
-// two, so bf16 values down to 2^-14 of the head's largest are exact), three
-// signed base-256 digits, int32 sums. e4m3: the rounding of q * S and the
-// rounding of 16 times what it left, which hold a bf16 value's 8 bits down to 2^-14
-// of the largest; fp32 sums. The decode group's few heads leave columns of the instruction
-// free, which the parts fill. P.V runs on fp16 instructions with fp32 sums:
-// codes are exact in fp16, weights rounded to fp16 (2^-11). V's scale joins the exponent: with
-// base-2 logits z and u_j = z_j + log2 sv_j, the weights a_j = 2^(u_j - M)
-// <= 2^8 multiply V's codes, and the sum of a_j / sv_j = 2^(z_j - M), in fp32
-// from the weights before their rounding, divides them at the end. One
-// reference M serves both, and it follows the running maximum of u lazily: only a value more
-// than 8 above it moves it, so the common tile takes no shuffle for the
-// maximum and no rescale.
+// Mathematics. Both products run on the 8-bit matrix instructions with the
+// codes as they lie in the cache, and the other operand cut into parts of the
+// cache's own type, which fill the columns that a decode group's few heads
+// leave free. q: in int8, q * S rounded to a 23-bit integer (S a power of two,
+// so bf16 values down to 2^-14 of the head's largest are exact), three signed base-256
+// digits; in e4m3, the rounding of q * S and the rounding of 16 times what it
+// left, which hold a bf16 value's 8 bits down to 2^-14 of the largest. The
+// weights: 24-bit fixed point as three unsigned bytes, or three e4m3 roundings, each
+// of 16 times what the one before left (12 bits). V's scale joins the
+// exponent: with base-2 logits z and u_j = z_j + log2 sv_j, the weights a_j =
+// 2^(u_j - M) < 2 multiply V's codes, and the sum of a_j / sv_j = 2^(z_j - M), in fp32
+// from the weights before they are cut up, divides them at the end. One
+// reference M serves both, and it follows the running maximum of u lazily:
+// only a value more than 0.9 above it moves it, so the common tile takes no
+// shuffle for the maximum and no rescale. int8 sums are int32 and join fp32
+// sums when M moves, and every kKaFoldTiles tiles, before they can overflow.
+// (Unpacking codes to fp16 instead took 80 to 140 integer instructions per 16 tokens, a third of
+// the loop, and left the fp16 instructions half empty.) Groups of more than 8
+// query heads would need more accumulators than there are registers: for
+// them P.V runs on fp16 instructions, with codes unpacked once for 16 heads
+// and weights rounded to fp16 (2^-11).
 //
 // Layout. Everything is warp-private: a warp owns up to 16 query heads of one
-// KV head and streams its tokens through a ring of 16-token cp.async stages
+// KV head and streams its tokens through a ring of 32-token cp.async stages
 // in shared memory; warps of a CTA take the heads of the same tokens, so that
 // a CTA's copies cover whole contiguous pool rows. There is no barrier
 // anywhere. Both products take the cache as the matrix instruction's A
 // operand (S^T = K Q^T and O^T = V^T P^T: M = 16 tokens or dims, N = 8
-// columns of heads and parts). The order of the contracted dims is free as
-// long as q and K agree, as is the order of V's dims, so each lane reads
-// 16-byte pieces of rows that are fragments already (K) or become some by
-// byte permutes (V); no transposing load is needed.
+// columns of heads and parts). K rows become fragments by a matrix load, V
+// rows by a transposing 8-bit matrix load, whose lanes get four consecutive
+// tokens of one dim; the tokens' order in the products is free, so row i of S
+// is the token for which the weights, transposed once, fall to the lanes that hold its codes.
 //
 // Split. The tokens of all requests form one list of 32-token tiles, cut into
 // equal ranges of one resident wave of CTAs; a range that crosses requests
@@ -47,10 +53,10 @@ namespace sd {
 
 constexpr int kKaThreads = 256;
 constexpr int kKaWarps = kKaThreads / 32;
-constexpr int kKaTile = 32;      // tokens per tile: one lookup per lane
-constexpr int kKaStep = 16;      // tokens per stage
-constexpr int kKaRanges = 296;   // CTAs of a column group in one wave: two per SM
-constexpr float kKaSlack = 8.f;  // log2: how far a weight may pass the running reference
+constexpr int kKaTile = 32;        // tokens per warp and stage: one row lookup per lane
+constexpr int kKaRanges = 148;     // CTAs of a column group in one wave: one per SM
+constexpr float kKaSlack = 0.9f;   // log2: how far a weight may pass the running reference
+constexpr int kKaFoldTiles = 1024; // int32 sums: 1024 x 32 x 255 x 128 < 2^31
 
 struct KvAttnArgs {
   const __nv_bfloat16* q;
@@ -71,20 +77,22 @@ struct KvAttnArgs {
 };
 
 // HPW: query heads per warp (4, 8 or 16). Lane (n, t) of a fragment holds the
-// logits of tokens n and n + 8 for kHL heads.
+// logits of kHL heads for the tokens of rows n and n + 8.
 template <int D, int HPW, int TYPE>
 struct KvAttnCfg {
+  static constexpr bool kBytes = HPW <= 8;  // P.V on 8-bit instructions
   static constexpr int kParts = TYPE == SD_KV_INT8 ? 3 : 2;
   // HPW 4: column 2t + x of S tile j is part 2j + x of head t; else tile
   // (hg, p) is part p of heads 8 hg .. 8 hg + 7
   static constexpr int kSTiles = HPW == 4 ? (kParts + 1) / 2 : HPW / 8 * kParts;
-  static constexpr int kOTiles = HPW == 4 ? 1 : HPW / 8;
+  // O likewise, with the three parts of the weights; fp16: head groups
+  static constexpr int kOTiles = HPW == 4 ? 2 : HPW == 8 ? 3 : 2;
   static constexpr int kHL = HPW == 4 ? 1 : HPW / 4;
-  static constexpr int kRowBytes = kKaStep * D;                   // K (or V) of a stage
-  static constexpr int kStage = 2 * kRowBytes + 2 * kKaStep * 4;  // + the tokens' scales
-  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kGroups = HPW == 16 ? 2 : 1;
+  static constexpr int kRowBytes = kKaTile * D;                   // K (or V) of a stage
+  static constexpr int kStage = 2 * kRowBytes + 2 * kKaTile * 4;  // + the tokens' scales
+  static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr size_t kSmem = (size_t)kKaWarps * kStages * kStage;
-  static constexpr int kCtas = HPW == 16 ? 1 : 2;                 // resident CTAs per SM
 };
 
 // Tokens (dense) or list slots of request b that the attention walks.
@@ -119,9 +127,15 @@ __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // m16n8k32 over 8-bit operands; d is four int32 (int8) or fp32 (e4m3) sums.
-template <int TYPE>
+// UNSIGNED: b holds unsigned bytes.
+template <int TYPE, bool UNSIGNED = false>
 __device__ __forceinline__ void mma_8bit_16832(uint32_t* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if constexpr (TYPE == SD_KV_INT8) {
+  if constexpr (TYPE == SD_KV_INT8 && UNSIGNED) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else if constexpr (TYPE == SD_KV_INT8) {
     asm volatile(
         "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
@@ -133,6 +147,20 @@ __device__ __forceinline__ void mma_8bit_16832(uint32_t* d, const uint32_t* a, u
         : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
+}
+__device__ __forceinline__ void ldmatrix_x4_at(uint32_t* r, uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+// Two 16 x 16 byte matrices, transposed: lane (n, t) gets bytes 4t .. 4t + 3 of
+// columns n (r[0], r[2]) and n + 8 (r[1], r[3]).
+__device__ __forceinline__ void ldmatrix_bytes_trans_x2(uint32_t* r, uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
@@ -201,6 +229,31 @@ __device__ __forceinline__ uint32_t q_part(const float* x, int p) {
   return w;
 }
 
+// Weights w < 1.9 in three bytes, the most significant part highest: 24-bit
+// fixed point, or e4m3 roundings of 128 w, of 16 times the rest and of 16 times that rest.
+template <int TYPE>
+__device__ __forceinline__ void weight_parts(float w0, float w1, uint32_t* p0, uint32_t* p1) {
+  if constexpr (TYPE == SD_KV_INT8) {
+    *p0 = __float2uint_rn(w0 * 8388608.f);
+    *p1 = __float2uint_rn(w1 * 8388608.f);
+  } else {
+    float2 x = make_float2(w0 * 128.f, w1 * 128.f);
+    uint32_t c[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      c[i] = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+      if (i == 2) break;
+      const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c[i]), __NV_E4M3)));
+      x.x = (x.x - y.x) * 16.f;
+      x.y = (x.y - y.y) * 16.f;
+    }
+    // c[i]: part i of w0 in byte 0, of w1 in byte 1
+    const uint32_t lo = c[2] | (c[1] << 16);
+    *p0 = __byte_perm(lo, c[0], 0x6420);  // part 2, part 1, part 0, zero
+    *p1 = __byte_perm(lo, c[0], 0x6531);
+  }
+}
+
 __device__ __forceinline__ int warp_inclusive_sum(int x) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -239,8 +292,7 @@ __device__ __forceinline__ int kv_attn_find(const KvAttnArgs& a, int t, int cnt,
 }
 
 template <int D, int HPW, int TYPE, bool LIST>
-__global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
-    kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
+__global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_constant__ KvAttnArgs a) {
   using C = KvAttnCfg<D, HPW, TYPE>;
   pdl_wait();  // inputs come from earlier work in the stream
   pdl_trigger();
@@ -258,7 +310,7 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
   const KvAttnCut cut(a, total);
   const int range = blockIdx.x;
   if (range >= cut.n || total == 0) return;
-  const int t_begin = cut.start(range), t_end = cut.start(range + 1);
+  const int t_begin = cut.start(range), my = cut.start(range + 1) - t_begin;  // tiles, one stage each
   int first;
   const int b_begin = kv_attn_find(a, t_begin, cnt, incl, &first);
   const int tile_begin = t_begin - first;
@@ -271,7 +323,6 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
   const int g = col / hblocks, h0 = g * a.qpk + (col % hblocks) * HPW;
   const int nh = min(HPW, (g + 1) * a.qpk - h0);
   unsigned char* ring = smem_raw + (size_t)warp * C::kStages * C::kStage;
-  const int my = 2 * (t_end - t_begin);  // stages: two per tile
 
   // ---- the copy side, one row per lane and tile, three steps ahead of each
   // other, so that a list entry, its page and its row are never waited for
@@ -330,52 +381,47 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
   constexpr int kPieces = D / 16;             // 16-byte pieces of a row
   constexpr int kRowsPerStep = 32 / kPieces;  // rows one copy instruction of the warp covers
   const int crow = lane / kPieces, cpiece = lane % kPieces;
-  // swizzles: see the reads below
+  // 16-byte piece c of token k's row lies at piece c ^ swizzle(k): the eight
+  // rows that one phase of a matrix load touches then fall into distinct banks
+  auto k_swizzle = [](int k) { return D == 128 ? (k & 1) | ((k >> 2) & 3) << 1 : (k >> 2) & 3; };
+  auto v_swizzle = [](int k) { return D == 128 ? k & 7 : (k >> 1) & 3; };
   const uint32_t ring_at = smem_u32(ring);
-  const uint32_t k_at = ring_at + crow * D + ((D == 128 ? cpiece ^ ((crow & 1) << 2) : cpiece) << 4);
-  const uint32_t v_at = ring_at + C::kRowBytes + crow * D +
-                        ((D == 128 ? cpiece ^ ((crow & 3) << 1) : cpiece ^ (((crow >> 1) & 1) << 1)) << 4);
   const uint8_t* k_src = a.k_pages + cpiece * 16;
   const uint8_t* v_src = a.v_pages + cpiece * 16;
-  uint32_t row16 = 0;   // this lane's row of the current tile, in 16-byte units; ~0: no token
-  long long scale_at = 0;
-  auto resolve = [&]() {
-    row16 = ~0u;
+  auto issue = [&](int stage) {
+    uint32_t row16 = ~0u;  // this lane's row, in 16-byte units; ~0: no token
+    const uint32_t base = ring_at + stage * C::kStage;
+    float* sc = reinterpret_cast<float*>(ring + stage * C::kStage + 2 * C::kRowBytes) + lane;
+    if (l2_ok && (l2_page < 0 || l2_page >= geo.num_pages)) {
+      raise_error(SD_DEVERR_PAGE);
+      l2_ok = false;
+    }
     if (l2_ok) {
-      if (l2_page >= 0 && l2_page < geo.num_pages) {
-        const int rid = l2_page * geo.page_size + l2_slot;
-        row16 = (static_cast<uint32_t>(rid) * G + g) * kPieces;
-        scale_at = (long long)geo.bs_div.div(rid) * G + g;
-      } else {
-        raise_error(SD_DEVERR_PAGE);
-      }
+      const int rid = l2_page * geo.page_size + l2_slot;
+      row16 = (static_cast<uint32_t>(rid) * G + g) * kPieces;
+      const size_t at = (size_t)geo.bs_div.div(rid) * G + g;
+      cp_async_4(sc, a.k_scales + at);
+      cp_async_4(sc + kKaTile, a.v_scales + at);
+    } else {
+      sc[0] = -1.f;  // no token here
+      sc[kKaTile] = 1.f;
     }
-  };
-  auto issue = [&](int stage, int half) {
-    const uint32_t off = stage * C::kStage;
-    const bool whole = __all_sync(0xffffffffu, row16 != ~0u);
+    const bool whole = __all_sync(0xffffffffu, l2_ok);
 #pragma unroll
-    for (int j = 0; j < kKaStep / kRowsPerStep; ++j) {
-      uint32_t row = __shfl_sync(0xffffffffu, row16, half * kKaStep + crow + j * kRowsPerStep);
-      int bytes = 16;
-      if (!whole) {  // 0 bytes: the piece is filled with zeros
-        bytes = row != ~0u ? 16 : 0;
-        row = row != ~0u ? row : 0u;
-      }
-      const size_t at = (size_t)row * 16;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(k_at + off + j * kRowsPerStep * D), "l"(k_src + at), "r"(bytes)
-                   : "memory");
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(v_at + off + j * kRowsPerStep * D), "l"(v_src + at), "r"(bytes)
-                   : "memory");
-    }
-    if (lane / kKaStep == half) {
-      float* sc = reinterpret_cast<float*>(ring + off + 2 * C::kRowBytes) + lane % kKaStep;
-      if (row16 != ~0u) {
-        cp_async_4(sc, a.k_scales + scale_at);
-        cp_async_4(sc + kKaStep, a.v_scales + scale_at);
-      } else {
-        sc[0] = -1.f;  // no token here
-        sc[kKaStep] = 1.f;
+    for (int j = 0; j < kKaTile / kRowsPerStep; ++j) {
+      const int k = crow + j * kRowsPerStep;
+      const uint32_t row = __shfl_sync(0xffffffffu, row16, k);
+      const uint32_t k_at = base + k * D + ((cpiece ^ k_swizzle(k)) << 4);
+      const uint32_t v_at = base + C::kRowBytes + k * D + ((cpiece ^ v_swizzle(k)) << 4);
+      if (whole) {
+        const size_t at = (size_t)row * 16;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(k_at), "l"(k_src + at) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(v_at), "l"(v_src + at) : "memory");
+      } else {  // rows without a token are filled with zeros
+        const int bytes = row != ~0u ? 16 : 0;
+        const size_t at = row != ~0u ? (size_t)row * 16 : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(k_at), "l"(k_src + at), "r"(bytes) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(v_at), "l"(v_src + at), "r"(bytes) : "memory");
       }
     }
   };
@@ -384,25 +430,42 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
   int cb = b_begin, ctile = tile_begin, clen = kv_attn_len(a, cb);
   uint32_t qf[C::kSTiles][D / 32][2];
   float qs[C::kHL];  // scale of this lane's heads (base-2 logits)
-  float o[C::kOTiles][D / 16][4];
   float m[C::kHL], l[C::kHL];
-  // head of this lane's logits, and of column n of S tile j (its part too)
+  uint32_t o[C::kOTiles][D / 16][4] = {};  // int32 or fp32 sums; D / 16 tiles of 16 dims
+  constexpr bool kFold = C::kBytes && TYPE == SD_KV_INT8;
+  float of[kFold ? C::kHL : 1][D / 16][2];  // what the int32 sums have been folded into
+  int since = 0;                            // tiles since then
   auto lane_head = [&](int i) { return HPW == 4 ? t : (i >> 1) * 8 + 2 * t + (i & 1); };
+  // sum of this lane's head i, dim 16 j + n + 8 x, in units of its weights and codes
+  auto sum_of = [&](int i, int j, int x) {
+    if constexpr (!C::kBytes) {
+      return __uint_as_float(o[i >> 1][j][2 * x + (i & 1)]);
+    } else {
+      const uint32_t p0 = HPW == 4 ? o[0][j][2 * x] : o[0][j][2 * x + (i & 1)];
+      const uint32_t p1 = HPW == 4 ? o[0][j][2 * x + 1] : o[1][j][2 * x + (i & 1)];
+      const uint32_t p2 = HPW == 4 ? o[1][j][2 * x] : o[C::kOTiles - 1][j][2 * x + (i & 1)];
+      if constexpr (TYPE == SD_KV_INT8)  // digits of 2^-23
+        return fmaf(static_cast<float>(static_cast<int>(p0)), 0.0078125f,
+                    fmaf(static_cast<float>(static_cast<int>(p1)), 0.0078125f / 256.f, static_cast<float>(static_cast<int>(p2)) * (0.0078125f / 65536.f)));
+      else
+        return fmaf(__uint_as_float(p0), 0.0078125f,
+                    fmaf(__uint_as_float(p1), 0.0078125f / 16.f, __uint_as_float(p2) * (0.0078125f / 256.f)));
+    }
+  };
   auto load_q = [&]() {
-    float back_of[C::kOTiles];  // scale of head n (HPW 4: n / 2) of head group j
+    float back_of[C::kGroups];  // scale of head n (HPW 4: n / 2) of head group j
 #pragma unroll
-    for (int hg = 0; hg < C::kOTiles; ++hg) {
+    for (int hg = 0; hg < C::kGroups; ++hg) {
       const int h = HPW == 4 ? n >> 1 : hg * 8 + n;
       const __nv_bfloat16* src = a.q + ((size_t)cb * a.H + h0 + (h < nh ? h : 0)) * D;
-      uint4 raw[D / 32];
+      uint32_t w[D / 8];  // dims 16 kk + 4t .. + 3 in words 2 kk, 2 kk + 1
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {  // piece t + 4j: 16 dims, 32 bytes
-        raw[2 * j] = *reinterpret_cast<const uint4*>(src + (t + 4 * j) * 16);
-        raw[2 * j + 1] = *reinterpret_cast<const uint4*>(src + (t + 4 * j) * 16 + 8);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint2 x = *reinterpret_cast<const uint2*>(src + kk * 16 + 4 * t);
+        w[2 * kk] = x.x, w[2 * kk + 1] = x.y;
       }
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
       float amax = 0.f;
-      bool bad = false;
+      int bad = 0;
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
         const float2 x = bf2(w[j]);
@@ -411,17 +474,17 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+      bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
       // up = 2^(e - floor(log2 amax)), as two factors since it can pass 2^127
       int ex = static_cast<int>(__float_as_uint(amax) >> 23);  // biased; 0: zero or subnormal
       ex = min(max(ex, 1), 254);
       const int up = (TYPE == SD_KV_INT8 ? 21 : 7) + 127 - ex;
       const float f0 = __uint_as_float((uint32_t)(up / 2 + 127) << 23), f1 = __uint_as_float((uint32_t)(up - up / 2 + 127) << 23);
-      back_of[hg] = a.scale_log2 / f0 / f1;
       // a query that is not finite makes its head's output NaN
-      if (__shfl_xor_sync(0xffffffffu, bad, 1) || bad) bad = true;
-      if (__shfl_xor_sync(0xffffffffu, bad, 2) || bad) back_of[hg] = __uint_as_float(0x7fc00000u);
+      back_of[hg] = bad ? __uint_as_float(0x7fc00000u) : a.scale_log2 / f0 / f1;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {  // word kk: dims of K's word kk
+      for (int kk = 0; kk < D / 16; ++kk) {
         const float2 x = bf2(w[2 * kk]), y = bf2(w[2 * kk + 1]);
         const float e[4] = {x.x * f0 * f1, x.y * f0 * f1, y.x * f0 * f1, y.y * f0 * f1};
         if constexpr (HPW == 4) {
@@ -433,14 +496,23 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
           for (int p = 0; p < C::kParts; ++p) qf[hg * C::kParts + p][kk / 2][kk % 2] = q_part<TYPE>(e, p);
         }
       }
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) o[hg][j][0] = o[hg][j][1] = o[hg][j][2] = o[hg][j][3] = 0.f;
     }
 #pragma unroll
     for (int i = 0; i < C::kHL; ++i) {
       qs[i] = __shfl_sync(0xffffffffu, back_of[HPW == 4 ? 0 : i >> 1], (HPW == 4 ? 2 * t : 2 * t + (i & 1)) * 4);
       m[i] = -INFINITY;
       l[i] = 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < C::kOTiles; ++h)
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) o[h][j][0] = o[h][j][1] = o[h][j][2] = o[h][j][3] = 0u;
+    if constexpr (kFold) {
+      since = 0;
+#pragma unroll
+      for (int i = 0; i < C::kHL; ++i)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) of[i][j][0] = of[i][j][1] = 0.f;
     }
   };
   auto flush = [&]() {
@@ -455,36 +527,39 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
       if (h >= nh) continue;
       const size_t at = slot * a.H + h0 + h;
       if (n == 0) a.part_ml[at] = make_float2(m[i], s);
-      // this lane's dims of the head: n * D/8 .. + D/8 - 1, dim 2j and 2j + 1 from m-tile j
-      float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + n * (D / 8));
-      const int hg = HPW == 4 ? 0 : i >> 1, x = HPW == 4 ? 0 : i & 1;
+      float* dst = a.part_o + at * D + n;
 #pragma unroll
-      for (int j = 0; j < D / 16; j += 2)
-        dst[j / 2] = make_float4(o[hg][j][x], o[hg][j][2 + x], o[hg][j + 1][x], o[hg][j + 1][2 + x]);
+      for (int j = 0; j < D / 16; ++j) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float v = sum_of(i, j, x);
+          if constexpr (kFold) v += of[i][j][x];
+          dst[16 * j + 8 * x] = v;
+        }
+      }
     }
   };
 
-  // A row i (= n, n + 8) of the stage is token pi(i): pi(2j) = j,
-  // pi(2j + 1) = (j + 4) ^ 1, + 8 for the upper half. It makes the rows that one
-  // phase of a shared load touches differ in the bits the swizzles use.
-  const int tk = (n & 1) ? (((n >> 1) + 4) ^ 1) : (n >> 1);
-  const int tv0 = t, tv1 = (t + 4) ^ 1;  // tokens pi(2t), pi(2t + 1)
+  // Row i of an S tile is token pi(i): rows 2j, 2j + 1 are tokens 4j, 4j + 1 and
+  // rows 8 + 2j, 9 + 2j tokens 4j + 2, 4j + 3. This lane's logits are tokens tk and
+  // tk + 2 (and 16 more for the second tile).
+  const int tk = 4 * (n >> 1) + (n & 1);
+  // this lane's row address in the matrix loads
+  const int k_row = 4 * ((lane >> 1) & 3) + (lane & 1) + 2 * ((lane >> 3) & 1);
+  const uint32_t k_read = ring_at + k_row * D, v_read = ring_at + C::kRowBytes + lane * D;
+  const int k_sw = k_swizzle(k_row), v_sw = v_swizzle(lane);  // rows 16 apart share a swizzle
 
-  // stage i is half i & 1 of tile i / 2; its tile is resolved when half 0 is issued
   auto feed = [&](int i, int stage) {
     if (i < my) {
-      if ((i & 1) == 0) {
-        resolve();
-        step2();
-        step1(i + 4 < my);
-      }
-      issue(stage, i & 1);
+      issue(stage);
+      step2();
+      step1(i + 2 < my);
     }
     cp_async_commit();
   };
   step1(my > 0);
   step2();
-  step1(my > 2);
+  step1(my > 1);
 #pragma unroll
   for (int s = 0; s < C::kStages - 1; ++s) feed(s, s);
   load_q();
@@ -493,63 +568,53 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
     cp_async_wait<C::kStages - 2>();
     __syncwarp();
     feed(at + C::kStages - 1, stage == 0 ? C::kStages - 1 : stage - 1);
-    const unsigned char* sk = ring + stage * C::kStage;
-    const unsigned char* sv = sk + C::kRowBytes;
-    const float* sc = reinterpret_cast<const float*>(sv + C::kRowBytes);
+    const uint32_t off = stage * C::kStage;
+    const float* sc = reinterpret_cast<const float*>(ring + off + 2 * C::kRowBytes);
 
-    // ---- S^T = K Q^T: 16 tokens x (heads and parts) ----
-    uint32_t s[C::kSTiles][4];
+    // ---- S^T = K Q^T: 2 x 16 tokens x (heads and parts) ----
+    uint32_t s[2][C::kSTiles][4];
 #pragma unroll
-    for (int j = 0; j < C::kSTiles; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0u;
+    for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const int piece = D == 128 ? (t + 4 * j) ^ ((tk & 1) << 2) : t;
-      const uint4 x = *reinterpret_cast<const uint4*>(sk + tk * D + piece * 16);
-      const uint4 y = *reinterpret_cast<const uint4*>(sk + (tk + 8) * D + piece * 16);
-      const uint32_t f0[4] = {x.x, y.x, x.y, y.y}, f1[4] = {x.z, y.z, x.w, y.w};
+      for (int j = 0; j < C::kSTiles; ++j) s[mt][j][0] = s[mt][j][1] = s[mt][j][2] = s[mt][j][3] = 0u;
 #pragma unroll
-      for (int h = 0; h < C::kSTiles; ++h) {
-        mma_8bit_16832<TYPE>(s[h], f0, qf[h][2 * j][0], qf[h][2 * j][1]);
-        mma_8bit_16832<TYPE>(s[h], f1, qf[h][2 * j + 1][0], qf[h][2 * j + 1][1]);
+      for (int j = 0; j < D / 32; ++j) {
+        uint32_t f[4];
+        ldmatrix_x4_at(f, k_read + off + mt * 16 * D + (((2 * j + (lane >> 4)) ^ k_sw) << 4));
+#pragma unroll
+        for (int h = 0; h < C::kSTiles; ++h) mma_8bit_16832<TYPE>(s[mt][h], f, qf[h][j][0], qf[h][j][1]);
       }
     }
 
-    // ---- weights of tokens n and n + 8 ----
-    float w[2][C::kHL];
-    bool over = false;
-    float isv[2];
+    // ---- weights: w[r] is token tk + 2 (r & 1) + 16 (r >> 1) ----
+    float w[4][C::kHL], isv[4];
+    bool over = kFold && ++since >= kKaFoldTiles;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float ks = sc[tk + 8 * r], vs = fmaxf(sc[kKaStep + tk + 8 * r], FLT_MIN);
+    for (int r = 0; r < 4; ++r) {
+      const int k = tk + 2 * (r & 1) + 16 * (r >> 1), x = 2 * (r & 1);
+      const float ks = sc[k], vs = fmaxf(sc[kKaTile + k], FLT_MIN);
       const float lv = fast_log2(vs);
       isv[r] = __fdividef(1.f, vs);
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i) {
-        // the parts of this lane's head i
+        const uint32_t(*p)[4] = s[r >> 1] + (HPW == 4 ? 0 : (i >> 1) * C::kParts);
+        const uint32_t p0 = HPW == 4 ? p[0][x] : p[0][x + (i & 1)], p1 = HPW == 4 ? p[0][x + 1] : p[1][x + (i & 1)];
         float z;
-        if constexpr (HPW == 4) {
-          if constexpr (TYPE == SD_KV_INT8)
-            z = fmaf(static_cast<float>(static_cast<int>(s[0][2 * r]) * 256 + static_cast<int>(s[0][2 * r + 1])), 256.f,
-                     static_cast<float>(static_cast<int>(s[1][2 * r])));
-          else
-            z = fmaf(__uint_as_float(s[0][2 * r + 1]), 0.0625f, __uint_as_float(s[0][2 * r]));
+        if constexpr (TYPE == SD_KV_INT8) {
+          const uint32_t p2 = HPW == 4 ? p[1][x] : p[C::kParts - 1][x + (i & 1)];
+          z = fmaf(static_cast<float>(static_cast<int>(p0) * 256 + static_cast<int>(p1)), 256.f, static_cast<float>(static_cast<int>(p2)));
         } else {
-          const uint32_t(*p)[4] = s + (i >> 1) * C::kParts;
-          const int x = 2 * r + (i & 1);
-          if constexpr (TYPE == SD_KV_INT8)
-            z = fmaf(static_cast<float>(static_cast<int>(p[0][x]) * 256 + static_cast<int>(p[1][x])), 256.f,
-                     static_cast<float>(static_cast<int>(p[2][x])));
-          else
-            z = fmaf(__uint_as_float(p[1][x]), 0.0625f, __uint_as_float(p[0][x]));
+          z = fmaf(__uint_as_float(p1), 0.0625f, __uint_as_float(p0));
         }
         w[r][i] = ks >= 0.f ? fmaf(z, qs[i] * ks, lv) : -INFINITY;  // u
         over |= w[r][i] > m[i] + kKaSlack;
       }
     }
     if (__any_sync(0xffffffffu, over)) {
+      since = 0;
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i) {
-        float mx = fmaxf(w[0][i], w[1][i]);
+        float mx = fmaxf(fmaxf(w[0][i], w[1][i]), fmaxf(w[2][i], w[3][i]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -557,71 +622,108 @@ __global__ void __launch_bounds__(kKaThreads, (KvAttnCfg<D, HPW, TYPE>::kCtas))
         const float alpha = mx == -INFINITY ? 1.f : fast_exp2(m[i] - mx);
         m[i] = mx;
         l[i] *= alpha;
-        const int hg = HPW == 4 ? 0 : i >> 1, x = HPW == 4 ? 0 : i & 1;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) o[hg][j][x] *= alpha, o[hg][j][2 + x] *= alpha;
+        for (int j = 0; j < D / 16; ++j) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if constexpr (kFold) {
+              of[i][j][x] = (of[i][j][x] + sum_of(i, j, x)) * alpha;
+            } else {
+#pragma unroll
+              for (int h = 0; h < C::kOTiles; ++h) {
+                if constexpr (!C::kBytes) {
+                  if (h == i >> 1) o[h][j][2 * x + (i & 1)] = __float_as_uint(__uint_as_float(o[h][j][2 * x + (i & 1)]) * alpha);
+                } else if constexpr (HPW == 4) {
+                  o[h][j][2 * x] = __float_as_uint(__uint_as_float(o[h][j][2 * x]) * alpha);
+                  if (h == 0) o[h][j][2 * x + 1] = __float_as_uint(__uint_as_float(o[h][j][2 * x + 1]) * alpha);
+                } else {
+                  o[h][j][2 * x + (i & 1)] = __float_as_uint(__uint_as_float(o[h][j][2 * x + (i & 1)]) * alpha);
+                }
+              }
+            }
+          }
+        }
+      }
+      if constexpr (kFold) {
+#pragma unroll
+        for (int h = 0; h < C::kOTiles; ++h)
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) o[h][j][0] = o[h][j][1] = o[h][j][2] = o[h][j][3] = 0u;
       }
     }
 #pragma unroll
     for (int i = 0; i < C::kHL; ++i) {
       const float ref = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < 4; ++r) {
         w[r][i] = fast_exp2(w[r][i] - ref);
         l[i] = fmaf(w[r][i], isv[r], l[i]);
       }
     }
-    uint32_t pf[C::kOTiles][2];
-#pragma unroll
-    for (int h = 0; h < C::kOTiles; ++h) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-        pf[h][r] = transpose_8x8(HPW == 4 ? pack_half2(w[r][0], 0.f) : pack_half2(w[r][2 * h], w[r][(2 * h + 1) % C::kHL]));
-    }
 
-    // ---- O^T += V^T P^T: D dims x heads; lane row n holds dims
-    // n * D/8 .. n * D/8 + D/8 - 1 of the tokens tv0, tv1 (+ 8) ----
-    constexpr int kVW = D / 32;  // 4-byte words of a lane's part of a V row
-    uint32_t va[4][kVW];
-    const int tok[4] = {tv0, tv1, tv0 + 8, tv1 + 8};
+    // ---- P: transposed so that a lane has its column's weights of the tokens
+    // 4t .. 4t + 3 (+ 16), whose codes it holds ----
+    if constexpr (C::kBytes) {
+      uint32_t pf[C::kOTiles][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(sv + tok[j] * D + ((n ^ ((tok[j] & 3) << 1)) << 4));
-        va[j][0] = x.x, va[j][1] = x.y, va[j][2] = x.z, va[j][3] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(sv + tok[j] * D + (((n >> 1) ^ (((tok[j] >> 1) & 1) << 1)) << 4) + (n & 1) * 8);
-        va[j][0] = x.x, va[j][1] = x.y;
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t p[2][C::kHL];  // parts of rows n and n + 8
+#pragma unroll
+        for (int i = 0; i < C::kHL; ++i) weight_parts<TYPE>(w[2 * mt][i], w[2 * mt + 1][i], &p[0][i], &p[1][i]);
+        if constexpr (HPW == 4) {
+          // 16-bit columns 2t: part 0 | part 2 << 8, 2t + 1: part 1
+          const uint32_t x = transpose_8x8(__byte_perm(p[0][0], 0u, 0x4102)), y = transpose_8x8(__byte_perm(p[1][0], 0u, 0x4102));
+          pf[0][mt] = __byte_perm(x, y, 0x6420);
+          pf[1][mt] = __byte_perm(x, y, 0x7531);
+        } else {
+          // columns 2t + i: part 0 | part 1 << 8 of head i; then part 2 of both rows
+          const uint32_t x = transpose_8x8(__byte_perm(p[0][0], p[0][C::kHL - 1], 0x5612));
+          const uint32_t y = transpose_8x8(__byte_perm(p[1][0], p[1][C::kHL - 1], 0x5612));
+          const uint32_t z = transpose_8x8(__byte_perm(__byte_perm(p[0][0], p[1][0], 0x0040), __byte_perm(p[0][C::kHL - 1], p[1][C::kHL - 1], 0x0040), 0x5410));
+          pf[0][mt] = __byte_perm(x, y, 0x6420);
+          pf[1][mt] = __byte_perm(x, y, 0x7531);
+          pf[C::kOTiles - 1][mt] = __byte_perm(z, 0u, 0x3120);
+        }
       }
-    }
+      // ---- O^T += V^T P^T: D dims x (heads and parts) ----
 #pragma unroll
-    for (int v = 0; v < kVW; ++v) {
-      // bytes of two tokens side by side: (tok0 dim d, tok1 dim d), ...
-      const uint32_t x0 = bias_codes<TYPE>(__byte_perm(va[0][v], va[1][v], 0x5140));
-      const uint32_t x1 = bias_codes<TYPE>(__byte_perm(va[0][v], va[1][v], 0x7362));
-      const uint32_t y0 = bias_codes<TYPE>(__byte_perm(va[2][v], va[3][v], 0x5140));
-      const uint32_t y1 = bias_codes<TYPE>(__byte_perm(va[2][v], va[3][v], 0x7362));
-      const uint32_t f0[4] = {codes_to_half2<TYPE, 0>(x0), codes_to_half2<TYPE, 1>(x0), codes_to_half2<TYPE, 0>(y0),
-                              codes_to_half2<TYPE, 1>(y0)};
-      const uint32_t f1[4] = {codes_to_half2<TYPE, 0>(x1), codes_to_half2<TYPE, 1>(x1), codes_to_half2<TYPE, 0>(y1),
-                              codes_to_half2<TYPE, 1>(y1)};
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t v[4];  // dims 16 j + n, + 8 of tokens 4t .. 4t + 3, then of 16 more
+        ldmatrix_bytes_trans_x2(v, v_read + off + ((j ^ v_sw) << 4));
 #pragma unroll
-      for (int h = 0; h < C::kOTiles; ++h) {
-        mma_f16_16816(o[h][2 * v], f0, pf[h][0], pf[h][1]);
-        mma_f16_16816(o[h][2 * v + 1], f1, pf[h][0], pf[h][1]);
+        for (int h = 0; h < C::kOTiles; ++h) mma_8bit_16832<TYPE, true>(o[h][j], v, pf[h][0], pf[h][1]);
+      }
+    } else {
+      uint32_t pf[C::kGroups][2][2];
+#pragma unroll
+      for (int h = 0; h < C::kGroups; ++h)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          pf[h][r >> 1][r & 1] = transpose_8x8(pack_half2(w[r][(2 * h) % C::kHL], w[r][(2 * h + 1) % C::kHL]));
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t v[4];
+        ldmatrix_bytes_trans_x2(v, v_read + off + ((j ^ v_sw) << 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = bias_codes<TYPE>(v[i]);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint32_t f[4] = {codes_to_half2<TYPE, 0>(v[2 * mt]), codes_to_half2<TYPE, 0>(v[2 * mt + 1]),
+                                 codes_to_half2<TYPE, 1>(v[2 * mt]), codes_to_half2<TYPE, 1>(v[2 * mt + 1])};
+#pragma unroll
+          for (int h = 0; h < C::kGroups; ++h) mma_f16_16816(reinterpret_cast<float*>(o[h][j]), f, pf[h][mt][0], pf[h][mt][1]);
+        }
       }
     }
 
     if (++stage == C::kStages) stage = 0;
-    if (at & 1) {
-      if ((++ctile) * a.spw * kKaTile >= clen || at + 1 == my) {  // the request or the range ends
-        flush();
-        if (at + 1 < my) {
-          ctile = 0;
-          do clen = kv_attn_len(a, ++cb);
-          while (clen == 0 && cb + 1 < a.B);
-          load_q();
-        }
+    if ((++ctile) * a.spw * kKaTile >= clen || at + 1 == my) {  // the request or the range ends
+      flush();
+      if (at + 1 < my) {
+        ctile = 0;
+        do clen = kv_attn_len(a, ++cb);
+        while (clen == 0 && cb + 1 < a.B);
+        load_q();
       }
     }
   }

@@ -1011,7 +1011,7 @@ KvAttnPlan kv_attn_plan(int B, int G, int H, int D) {
   p.cols = G * sd::ceil_div(qpk, p.hpw);
   p.col_groups = sd::ceil_div(p.cols, sd::kKaWarps);
   p.spw = p.cols >= sd::kKaWarps ? 1 : sd::kKaWarps / p.cols;
-  p.ranges = std::max(1, sd::kKaRanges / (p.hpw == 16 ? 2 : 1) / p.col_groups);
+  p.ranges = std::max(1, sd::kKaRanges / p.col_groups);
   const size_t rows = ((size_t)p.ranges + B) * p.spw * H;
   p.off_ml = align_up(rows * D * sizeof(float));
   p.total = p.off_ml + align_up(rows * sizeof(float2));
