@@ -204,29 +204,31 @@ __device__ __forceinline__ uint32_t bias_codes(uint32_t w) {
   return TYPE == SD_KV_INT8 ? w ^ 0x80808080u : w;
 }
 
-// Part p of four elements of q (already times the head's power of two).
+// The parts of four elements of q (already times the head's power of two), one
+// word per part, the most significant first.
 template <int TYPE>
-__device__ __forceinline__ uint32_t q_part(const float* x, int p) {
-  uint32_t w = 0;
+__device__ __forceinline__ void q_parts(const float* x, uint32_t* w) {
+  if constexpr (TYPE == SD_KV_INT8) {
+    // |f| <= 2^22; the bytes of f + 0x808080 are its digits in [-128, 127] plus 128
+    uint32_t f[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if constexpr (TYPE == SD_KV_INT8) {
-      int f = __float2int_rn(x[j]);  // |f| <= 2^22
+    for (int j = 0; j < 4; ++j) f[j] = static_cast<uint32_t>(__float2int_rn(x[j]) + 0x808080) ^ 0x808080u;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {  // digits from the low end: part 2, 1, 0
-        const int d = static_cast<int8_t>(f & 0xff);
-        if (p == 2 - i) w |= static_cast<uint32_t>(d & 0xff) << (8 * j);
-        f = (f - d) >> 8;
-      }
-      if (p == 0) w |= static_cast<uint32_t>(f & 0xff) << (8 * j);
-    } else {
-      const __nv_fp8_storage_t a = __nv_cvt_float_to_fp8(x[j], __NV_SATFINITE, __NV_E4M3);
-      const float rest = (x[j] - __half2float(__half(__nv_cvt_fp8_to_halfraw(a, __NV_E4M3)))) * 16.f;
-      const __nv_fp8_storage_t b = __nv_cvt_float_to_fp8(rest, __NV_SATFINITE, __NV_E4M3);
-      w |= static_cast<uint32_t>(p == 0 ? a : b) << (8 * j);
+    for (int p = 0; p < 3; ++p) {
+      const uint32_t sel = p == 0 ? 0x0062u : p == 1 ? 0x0051u : 0x0040u;
+      w[p] = __byte_perm(__byte_perm(f[0], f[1], sel), __byte_perm(f[2], f[3], sel), 0x5410);
     }
+  } else {
+    uint32_t c[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      c[0][j] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * j], x[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+      const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c[0][j]), __NV_E4M3)));
+      c[1][j] = __nv_cvt_float2_to_fp8x2(make_float2((x[2 * j] - y.x) * 16.f, (x[2 * j + 1] - y.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) w[p] = c[p][0] | (c[p][1] << 16);
   }
-  return w;
 }
 
 // Weights w < 1.9 in three bytes, the most significant part highest: 24-bit
@@ -452,48 +454,49 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
                     fmaf(__uint_as_float(p1), 0.0078125f / 16.f, __uint_as_float(p2) * (0.0078125f / 256.f)));
     }
   };
-  auto load_q = [&]() {
-    float back_of[C::kGroups];  // scale of head n (HPW 4: n / 2) of head group j
+  uint32_t qraw[C::kGroups][D / 8];  // dims 16 kk + 4t .. + 3 in words 2 kk, 2 kk + 1 of head n (HPW 4: n / 2)
+  auto fetch_q = [&](int b) {
 #pragma unroll
     for (int hg = 0; hg < C::kGroups; ++hg) {
       const int h = HPW == 4 ? n >> 1 : hg * 8 + n;
-      const __nv_bfloat16* src = a.q + ((size_t)cb * a.H + h0 + (h < nh ? h : 0)) * D;
-      uint32_t w[D / 8];  // dims 16 kk + 4t .. + 3 in words 2 kk, 2 kk + 1
+      const __nv_bfloat16* src = a.q + ((size_t)b * a.H + h0 + (h < nh ? h : 0)) * D;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint2 x = *reinterpret_cast<const uint2*>(src + kk * 16 + 4 * t);
-        w[2 * kk] = x.x, w[2 * kk + 1] = x.y;
+        qraw[hg][2 * kk] = x.x, qraw[hg][2 * kk + 1] = x.y;
       }
-      float amax = 0.f;
-      int bad = 0;
+    }
+  };
+  auto begin_request = [&]() {
+    float back_of[C::kGroups];  // scale of qraw's heads
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        const float2 x = bf2(w[j]);
-        amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
-        bad |= !(fabsf(x.x) <= FLT_MAX) || !(fabsf(x.y) <= FLT_MAX);
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-      bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+    for (int hg = 0; hg < C::kGroups; ++hg) {
+      const uint32_t* w = qraw[hg];
+      // the largest magnitude, as the bits of the bf16s: that of a value that
+      // is not finite is above all others
+      uint32_t top = 0u;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) top = max(top, max(w[j] & 0x7fff0000u, (w[j] << 16) & 0x7fff0000u));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // up = 2^(e - floor(log2 amax)), as two factors since it can pass 2^127
-      int ex = static_cast<int>(__float_as_uint(amax) >> 23);  // biased; 0: zero or subnormal
-      ex = min(max(ex, 1), 254);
+      const int ex = min(max(static_cast<int>(top >> 23), 1), 254);  // biased; 0: zero or subnormal
       const int up = (TYPE == SD_KV_INT8 ? 21 : 7) + 127 - ex;
       const float f0 = __uint_as_float((uint32_t)(up / 2 + 127) << 23), f1 = __uint_as_float((uint32_t)(up - up / 2 + 127) << 23);
       // a query that is not finite makes its head's output NaN
-      back_of[hg] = bad ? __uint_as_float(0x7fc00000u) : a.scale_log2 / f0 / f1;
+      back_of[hg] = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : a.scale_log2 / f0 / f1;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const float2 x = bf2(w[2 * kk]), y = bf2(w[2 * kk + 1]);
         const float e[4] = {x.x * f0 * f1, x.y * f0 * f1, y.x * f0 * f1, y.y * f0 * f1};
+        uint32_t p[C::kParts];
+        q_parts<TYPE>(e, p);
         if constexpr (HPW == 4) {
-          const uint32_t p0 = q_part<TYPE>(e, 0), p1 = q_part<TYPE>(e, 1);
-          qf[0][kk / 2][kk % 2] = n & 1 ? p1 : p0;
-          if constexpr (C::kSTiles == 2) qf[1][kk / 2][kk % 2] = n & 1 ? 0u : q_part<TYPE>(e, 2);
+          qf[0][kk / 2][kk % 2] = n & 1 ? p[1] : p[0];
+          if constexpr (C::kSTiles == 2) qf[1][kk / 2][kk % 2] = n & 1 ? 0u : p[2];
         } else {
 #pragma unroll
-          for (int p = 0; p < C::kParts; ++p) qf[hg * C::kParts + p][kk / 2][kk % 2] = q_part<TYPE>(e, p);
+          for (int i = 0; i < C::kParts; ++i) qf[hg * C::kParts + i][kk / 2][kk % 2] = p[i];
         }
       }
     }
@@ -515,8 +518,8 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
         for (int j = 0; j < D / 16; ++j) of[i][j][0] = of[i][j][1] = 0.f;
     }
   };
-  auto flush = [&]() {
-    const size_t slot = ((size_t)range + cb) * a.spw + sub;
+  auto flush = [&](int b) {
+    const size_t slot = ((size_t)range + b) * a.spw + sub;
 #pragma unroll
     for (int i = 0; i < C::kHL; ++i) {
       float s = l[i];
@@ -557,12 +560,34 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
     }
     cp_async_commit();
   };
-  step1(my > 0);
-  step2();
-  step1(my > 1);
+  // the first tiles' lookups side by side, one trip for all at each step
+  {
+    fetch_q(b_begin);
+    constexpr int kAhead = C::kStages - 1;
+    int tok[kAhead], rem[kAhead], rb[kAhead], rL[kAhead], page[kAhead], slot[kAhead];
+    bool ok[kAhead];
 #pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) feed(s, s);
-  load_q();
+    for (int i = 0; i < kAhead; ++i) {
+      step1(i < my);
+      tok[i] = l1_tok, rem[i] = l1_rem, rb[i] = l1_b, rL[i] = l1_L;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      l1_tok = tok[i], l1_rem = rem[i], l1_b = rb[i], l1_L = rL[i];
+      step2();
+      page[i] = l2_page, slot[i] = l2_slot, ok[i] = l2_ok;
+    }
+    step1(kAhead < my);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      l2_page = page[i], l2_slot = slot[i], l2_ok = ok[i];
+      if (i < my) issue(i);
+      cp_async_commit();
+    }
+    step2();
+    step1(kAhead + 1 < my);
+  }
+  begin_request();
   int stage = 0;
   for (int at = 0; at < my; ++at) {
     cp_async_wait<C::kStages - 2>();
@@ -718,13 +743,15 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
 
     if (++stage == C::kStages) stage = 0;
     if ((++ctile) * a.spw * kKaTile >= clen || at + 1 == my) {  // the request or the range ends
-      flush();
+      const int done = cb;
       if (at + 1 < my) {
         ctile = 0;
         do clen = kv_attn_len(a, ++cb);
         while (clen == 0 && cb + 1 < a.B);
-        load_q();
+        fetch_q(cb);
       }
+      flush(done);
+      if (at + 1 < my) begin_request();
     }
   }
   cp_async_wait<0>();
