@@ -14,9 +14,11 @@
 // q carries 2^800 and the result 2^96 to make up for it.
 //
 // Split of the scores: D / 4 lanes share a block, four dims each, so that a
-// lane keeps its dims of four query heads in registers and reads the bounds
-// straight from global memory; the sums of four blocks and four heads are
-// reduced over the lanes together, halving their number at each step. Bound
+// lane keeps its dims of four query heads in registers; the bounds stream
+// through a ring of cp.async stages of the warp's own (read straight into
+// registers, too few of them were in flight: 39 against 31 us for 131072
+// blocks); the sums of four blocks and four heads are reduced over the lanes
+// together, halving their number at each step. Bound
 // by HBM (4 D bytes per block and KV head) up to four query heads per KV
 // head, and by issue slots above.
 //
@@ -37,6 +39,7 @@ constexpr int kBtThreads = 32 * kBtWarps;
 constexpr int kBtHeads = 4;   // query heads summed at once
 constexpr int kBtBatch = 4;   // blocks a lane group has in flight
 constexpr int kBtChunk = 32;  // most blocks per warp
+constexpr int kBtStages = 5;  // batches in the ring
 
 struct BlockScoreArgs {
   const __nv_bfloat16 *q, *bounds;
@@ -59,7 +62,9 @@ __device__ __forceinline__ uint32_t bf16_hi_scaled_hi(uint32_t w) {
 template <int D>
 __global__ void __launch_bounds__(kBtThreads, 4) block_score_kernel(const __grid_constant__ BlockScoreArgs a) {
   constexpr int LANES = D / 4, GROUPS = 32 / LANES, STEP = GROUPS * kBtBatch;
-  __shared__ float s_best[kBtWarps][kBtChunk];
+  constexpr int kRow = 4 * D;  // bytes of a block's bounds: lo, hi
+  __shared__ __align__(16) unsigned char s_ring[kBtWarps][kBtStages][STEP * kRow];
+  __shared__ float s_best[kBtWarps][32];
   const KvGeom& geo = a.geo;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / LANES, l = lane % LANES;
   const int g = blockIdx.y % geo.G, b = blockIdx.y / geo.G;
@@ -99,23 +104,35 @@ __global__ void __launch_bounds__(kBtThreads, 4) block_score_kernel(const __grid
         pick[h][d] = e[d] < 0.f ? 0x3210u : 0x7654u;
       }
     }
-    for (int i0 = 0; i0 < a.chunk && c0 + i0 < count; i0 += STEP) {
-      uint2 lo[kBtBatch], hi[kBtBatch];
+    const int end = min(a.chunk, count - c0);
+    auto feed = [&](int i0, int stage) {  // blocks i0 .. i0 + STEP - 1
+      if (i0 < end) {
+        constexpr int kPerCopy = 512 / kRow;  // rows that one copy of the warp covers
 #pragma unroll
-      for (int i = 0; i < kBtBatch; ++i) {
-        const int at = __shfl_sync(0xffffffffu, blk, i0 + grp * kBtBatch + i);
-        lo[i] = hi[i] = make_uint2(0u, 0u);
-        if (at >= 0) {
-          const __nv_bfloat16* src = a.bounds + ((long long)at * geo.G + g) * (2 * D) + 4 * l;
-          lo[i] = *reinterpret_cast<const uint2*>(src);
-          hi[i] = *reinterpret_cast<const uint2*>(src + D);
+        for (int i = 0; i < STEP / kPerCopy; ++i) {
+          const int r = i * kPerCopy + lane / (32 / kPerCopy), piece = lane % (32 / kPerCopy);
+          const int at = __shfl_sync(0xffffffffu, blk, (i0 + r) & 31);
+          cp_async_16(s_ring[warp][stage] + r * kRow + piece * 16,
+                      a.bounds + ((long long)max(at, 0) * geo.G + g) * (2 * D) + piece * 8, at >= 0 ? 16 : 0);
         }
       }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kBtStages - 1; ++i) feed(i * STEP, i);
+    int stage = 0;
+    for (int i0 = 0; i0 < end; i0 += STEP) {
+      cp_async_wait<kBtStages - 2>();
+      __syncwarp();
+      feed(i0 + (kBtStages - 1) * STEP, stage == 0 ? kBtStages - 1 : stage - 1);
+      const unsigned char* rows = s_ring[warp][stage] + grp * kBtBatch * kRow + 8 * l;
+      stage = stage + 1 == kBtStages ? 0 : stage + 1;
       double v[kBtBatch * kBtHeads];
 #pragma unroll
       for (int i = 0; i < kBtBatch; ++i) {
-        const uint32_t kl[4] = {bf16_lo_scaled_hi(lo[i].x), bf16_hi_scaled_hi(lo[i].x), bf16_lo_scaled_hi(lo[i].y), bf16_hi_scaled_hi(lo[i].y)};
-        const uint32_t kh[4] = {bf16_lo_scaled_hi(hi[i].x), bf16_hi_scaled_hi(hi[i].x), bf16_lo_scaled_hi(hi[i].y), bf16_hi_scaled_hi(hi[i].y)};
+        const uint2 lo = *reinterpret_cast<const uint2*>(rows + i * kRow), hi = *reinterpret_cast<const uint2*>(rows + i * kRow + 2 * D);
+        const uint32_t kl[4] = {bf16_lo_scaled_hi(lo.x), bf16_hi_scaled_hi(lo.x), bf16_lo_scaled_hi(lo.y), bf16_hi_scaled_hi(lo.y)};
+        const uint32_t kh[4] = {bf16_lo_scaled_hi(hi.x), bf16_hi_scaled_hi(hi.x), bf16_lo_scaled_hi(hi.y), bf16_hi_scaled_hi(hi.y)};
 #pragma unroll
         for (int h = 0; h < kBtHeads; ++h) {
           double s = 0.0;
@@ -154,6 +171,8 @@ __global__ void __launch_bounds__(kBtThreads, 4) block_score_kernel(const __grid
         if (i < a.chunk) s_best[warp][i] = fmaxf(s_best[warp][i], f);
       }
     }
+    cp_async_wait<0>();
+    __syncwarp();  // the ring is free for the next heads
   }
   __syncwarp();
   if (lane >= a.chunk || c >= count) return;
