@@ -63,7 +63,7 @@ struct KvStoreArgs {
   int R;
   bool interleaved;
   __nv_bfloat16* q_out;
-  int kv_ctas, heads_per_group, head_groups;
+  int kv_ctas, q_ctas, heads_per_group, head_groups;
   bool by_row;  // unit u is row u (where every row can start a block), else the u-th touched block
 };
 
@@ -187,6 +187,7 @@ struct Rotation {
   }
 };
 
+// Four codes round(e * inv), any input: NaN is 0, infinities the largest code.
 __device__ __forceinline__ uint32_t encode4(const float* e, float inv, int kv_type) {
   if (kv_type == SD_KV_INT8) {
     uint32_t w = 0;
@@ -205,6 +206,20 @@ __device__ __forceinline__ uint32_t encode4(const float* e, float inv, int kv_ty
   }
   const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(z[0], z[1]), __NV_SATFINITE, __NV_E4M3);
   const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(z[2], z[3]), __NV_SATFINITE, __NV_E4M3);
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// The same for finite e with |e * inv| <= 127 in int8: adding 1.5 * 2^23
+// rounds to a whole number (to even) whose low byte is the code.
+__device__ __forceinline__ uint32_t encode4_finite(const float* e, float inv, int kv_type) {
+  if (kv_type == SD_KV_INT8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(fmaf(e[j], inv, 12582912.f));
+    return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+  }
+  const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(e[0] * inv, e[1] * inv), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(e[2] * inv, e[3] * inv), __NV_SATFINITE, __NV_E4M3);
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
@@ -245,7 +260,7 @@ __device__ __forceinline__ void recode_rows(uint8_t* first, long long pitch, int
   }
 }
 
-template <int D>
+template <int D, bool FINITE = false>
 __device__ __forceinline__ void store_row(void* pages, long long row, int l, const float* e, float inv, int kv_type) {
   if (kv_type == SD_KV_BF16) {
     __nv_bfloat16* at = static_cast<__nv_bfloat16*>(pages) + row * D;
@@ -253,8 +268,8 @@ __device__ __forceinline__ void store_row(void* pages, long long row, int l, con
     *reinterpret_cast<uint2*>(at + D / 2 + 4 * l) = make_uint2(pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7]));
   } else {
     uint8_t* at = static_cast<uint8_t*>(pages) + row * D;
-    *reinterpret_cast<uint32_t*>(at + 4 * l) = encode4(e, inv, kv_type);
-    *reinterpret_cast<uint32_t*>(at + D / 2 + 4 * l) = encode4(e + 4, inv, kv_type);
+    *reinterpret_cast<uint32_t*>(at + 4 * l) = FINITE ? encode4_finite(e, inv, kv_type) : encode4(e, inv, kv_type);
+    *reinterpret_cast<uint32_t*>(at + D / 2 + 4 * l) = FINITE ? encode4_finite(e + 4, inv, kv_type) : encode4(e + 4, inv, kv_type);
   }
 }
 
@@ -271,10 +286,10 @@ __device__ __forceinline__ int row_position(const KvStoreArgs& a, int b, int r, 
 }
 
 template <int D, bool FULL>
-__device__ void store_queries(const KvStoreArgs& a) {
+__device__ void store_queries(const KvStoreArgs& a, int cta) {
   constexpr int LANES = D / 8, GROUPS = kKvThreads / LANES;
   const int l = threadIdx.x % LANES;
-  const int item = (blockIdx.x - a.kv_ctas) * GROUPS + threadIdx.x / LANES;
+  const int item = cta * GROUPS + threadIdx.x / LANES;
   const int token = item / a.head_groups, hg = item - token * a.head_groups;
   const bool in = token < a.T;
   const int b = find_request<LANES>(a.tok_start, a.B, in ? token : 0, l);
@@ -327,9 +342,11 @@ struct KvUnit {
   bool ok;
 };
 
-// Block c of request b with new positions [p0, p1), whose first is row r0. `raise`: whether this
-// thread reports bad data.
-__device__ __forceinline__ KvUnit make_unit(const KvStoreArgs& a, int b, int c, int r0, int p0, int p1, int g, bool raise) {
+// Block c of request b with new positions [p0, p1), whose first is row r0.
+// `raise`: whether this thread reports bad data. `begin(row0, nr)` is called
+// before the page is looked up.
+template <class Begin>
+__device__ __forceinline__ KvUnit make_unit(const KvStoreArgs& a, int b, int c, int r0, int p0, int p1, int g, bool raise, Begin begin) {
   const KvGeom& geo = a.geo;
   KvUnit u;
   u.b = b, u.c = c, u.ok = false;
@@ -341,6 +358,7 @@ __device__ __forceinline__ KvUnit make_unit(const KvStoreArgs& a, int b, int c, 
     if (raise) raise_error(SD_DEVERR_INDEX);
     return u;
   }
+  begin(u.row0, u.nr);
   const int pi = geo.page_div.div(c * geo.bs);
   const int page = a.block_table[(size_t)b * geo.max_pages + pi];
   if (page < 0 || page >= geo.num_pages) {
@@ -356,17 +374,39 @@ __device__ __forceinline__ KvUnit make_unit(const KvStoreArgs& a, int b, int c, 
 
 template <int D>
 struct KvBlockSmem {
-  float amax[2][kKvThreads / 32];
-  float bounds[2][kKvThreads / 32][D];
+  uint32_t amax[2][kKvThreads / 32];
+  __nv_bfloat16 bounds[2][kKvThreads / 32][D];
   int scan[kKvThreads / 32];
   int unit[2];
   KvUnit units[kKvThreads / 32];
 };
 
-// A unit of any number of rows, by the whole CTA. `rows` holds block_tokens x
-// D floats of the rotated K.
+// The new rows of a unit, K and V, on their way to shared memory. A lane
+// copies what it reads later, so its own wait is all that is needed: its K
+// elements go to where their fp32 values will stand.
+template <int D>
+__device__ __forceinline__ void copy_unit_rows(const KvStoreArgs& a, int row0, int nr, int g, float* rows, __nv_bfloat16* vrows) {
+  constexpr int LANES = D / 8, RPP = kKvThreads / LANES;
+  const int l = threadIdx.x % LANES;
+  const __nv_bfloat16* ks = a.k + row0 * a.k_stride + (long long)g * D + 4 * l;
+  const __nv_bfloat16* vs = a.v + row0 * a.v_stride + (long long)g * D + 4 * l;
+#pragma unroll 2
+  for (int i = threadIdx.x / LANES; i < nr; i += RPP) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(rows + i * D + h * (D / 2) + 4 * l)),
+                   "l"(ks + i * a.k_stride + h * (D / 2)) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(vrows + i * D + h * (D / 2) + 4 * l)),
+                   "l"(vs + i * a.v_stride + h * (D / 2)) : "memory");
+    }
+  }
+  cp_async_commit();
+}
+
+// A unit of any number of rows, by the whole CTA, once its rows are under way
+// to `rows` (block_tokens x D floats) and `vrows` (as many bf16).
 template <int D, bool FULL>
-__device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBlockSmem<D>& sm, float* rows) {
+__device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBlockSmem<D>& sm, float* rows, __nv_bfloat16* vrows) {
   constexpr int LANES = D / 8, RPP = kKvThreads / LANES;
   const KvGeom& geo = a.geo;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = tid % LANES, bs = geo.bs;
@@ -376,21 +416,25 @@ __device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBl
   rot.init(a.inv_freq, a.R, a.interleaved, l);
   float w[8];
   if (a.kw != nullptr) load_weight<D>(a.kw, l, w);
-  const __nv_bfloat16* ks = a.k + u.row0 * a.k_stride + (long long)g * D + 4 * l;
-  const __nv_bfloat16* vs = a.v + u.row0 * a.v_stride + (long long)g * D + 4 * l;
-  float mk = 0.f, mv = 0.f, bmin[8], bmax[8];
+  // largest magnitudes as bits (of fp32 for K, of bf16 pairs for V): those of
+  // entries that are not finite are above all others
+  uint32_t mk = 0u, mv = 0u;
+  __nv_bfloat162 bmin[4], bmax[4];  // of bf16(y); NaN drops out
 #pragma unroll
-  for (int j = 0; j < 8; ++j) bmin[j] = INFINITY, bmax[j] = -INFINITY;
+  for (int j = 0; j < 4; ++j) bmin[j] = __float2bfloat162_rn(INFINITY), bmax[j] = __float2bfloat162_rn(-INFINITY);
+  cp_async_wait<0>();
 #pragma unroll 1
   for (int i0 = 0; i0 < u.nr; i0 += RPP) {
     const int i = i0 + tid / LANES;
     const bool in = i < u.nr;
+    float* at = rows + i * D + 4 * l;
+    const __nv_bfloat16* vat = vrows + i * D + 4 * l;
     uint2 x = make_uint2(0u, 0u), y = x, vx = x, vy = x;
     if (in) {
-      x = *reinterpret_cast<const uint2*>(ks + i * a.k_stride);
-      y = *reinterpret_cast<const uint2*>(ks + i * a.k_stride + D / 2);
-      vx = *reinterpret_cast<const uint2*>(vs + i * a.v_stride);
-      vy = *reinterpret_cast<const uint2*>(vs + i * a.v_stride + D / 2);
+      x = *reinterpret_cast<const uint2*>(at);
+      y = *reinterpret_cast<const uint2*>(at + D / 2);
+      vx = *reinterpret_cast<const uint2*>(vat);
+      vy = *reinterpret_cast<const uint2*>(vat + D / 2);
     }
     float e[8];
     unpack_row<D>(x, y, e);
@@ -400,55 +444,71 @@ __device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBl
       rot.apply(e, a.R, a.interleaved, l);
     }
     if (in) {
-      float v[8];
-      unpack_row<D>(vx, vy, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mk = fmaxf(mk, finite_abs(e[j]));
-        mv = fmaxf(mv, finite_abs(v[j]));
-        const float kb = __bfloat162float(__float2bfloat16_rn(e[j]));
-        bmin[j] = fminf(bmin[j], kb);
-        bmax[j] = fmaxf(bmax[j], kb);
+      for (int j = 0; j < 4; ++j) {
+        mk = max(mk, max(__float_as_uint(e[2 * j]) & 0x7fffffffu, __float_as_uint(e[2 * j + 1]) & 0x7fffffffu));
+        const __nv_bfloat162 kb = __floats2bfloat162_rn(e[2 * j], e[2 * j + 1]);
+        bmin[j] = __hmin2(bmin[j], kb);
+        bmax[j] = __hmax2(bmax[j], kb);
       }
+      mv = __vmaxu2(mv, __vmaxu2(__vmaxu2(vx.x & 0x7fff7fffu, vx.y & 0x7fff7fffu), __vmaxu2(vy.x & 0x7fff7fffu, vy.y & 0x7fff7fffu)));
       if (quant) {
-        *reinterpret_cast<float4*>(rows + i * D + 4 * l) = make_float4(e[0], e[1], e[2], e[3]);
-        *reinterpret_cast<float4*>(rows + i * D + D / 2 + 4 * l) = make_float4(e[4], e[5], e[6], e[7]);
+        *reinterpret_cast<float4*>(at) = make_float4(e[0], e[1], e[2], e[3]);
+        *reinterpret_cast<float4*>(at + D / 2) = make_float4(e[4], e[5], e[6], e[7]);
       } else {
         const long long row = (u.base + (u.lo - u.c * bs) + i) * geo.G + g;
         store_row<D>(a.k_pages, row, l, e, 1.f, SD_KV_BF16);
-        store_row<D>(a.v_pages, row, l, v, 1.f, SD_KV_BF16);
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.v_pages) + row * D + 4 * l;
+        *reinterpret_cast<uint2*>(dst) = vx;
+        *reinterpret_cast<uint2*>(dst + D / 2) = vy;
       }
     }
   }
   if (quant) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-      mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-    }
+    mv = max(mv & 0xffffu, mv >> 16) << 16;
+    mk = __reduce_max_sync(0xffffffffu, mk);
+    mv = __reduce_max_sync(0xffffffffu, mv);
     if (lane == 0) sm.amax[0][warp] = mk, sm.amax[1][warp] = mv;
   }
   if (a.bounds != nullptr) {
 #pragma unroll
     for (int o = LANES; o < 32; o <<= 1) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        bmin[j] = fminf(bmin[j], __shfl_xor_sync(0xffffffffu, bmin[j], o));
-        bmax[j] = fmaxf(bmax[j], __shfl_xor_sync(0xffffffffu, bmax[j], o));
+      for (int j = 0; j < 4; ++j) {
+        bmin[j] = __hmin2(bmin[j], __shfl_xor_sync(0xffffffffu, bmin[j], o));
+        bmax[j] = __hmax2(bmax[j], __shfl_xor_sync(0xffffffffu, bmax[j], o));
       }
     }
     if (lane < LANES) {
-      *reinterpret_cast<float4*>(&sm.bounds[0][warp][4 * l]) = make_float4(bmin[0], bmin[1], bmin[2], bmin[3]);
-      *reinterpret_cast<float4*>(&sm.bounds[0][warp][D / 2 + 4 * l]) = make_float4(bmin[4], bmin[5], bmin[6], bmin[7]);
-      *reinterpret_cast<float4*>(&sm.bounds[1][warp][4 * l]) = make_float4(bmax[0], bmax[1], bmax[2], bmax[3]);
-      *reinterpret_cast<float4*>(&sm.bounds[1][warp][D / 2 + 4 * l]) = make_float4(bmax[4], bmax[5], bmax[6], bmax[7]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = (j < 2 ? 0 : D / 2 - 4) + 4 * l + 2 * j;
+        *reinterpret_cast<__nv_bfloat162*>(&sm.bounds[0][warp][d]) = bmin[j];
+        *reinterpret_cast<__nv_bfloat162*>(&sm.bounds[1][warp][d]) = bmax[j];
+      }
     }
   }
   __syncthreads();  // also: every thread has read the old scales
   if (quant) {
-    for (int i = 0; i < kKvThreads / 32; ++i) mk = fmaxf(mk, sm.amax[0][i]), mv = fmaxf(mv, sm.amax[1][i]);
+    for (int i = 0; i < kKvThreads / 32; ++i) mk = max(mk, sm.amax[0][i]), mv = max(mv, sm.amax[1][i]);
+    const bool finite = max(mk, mv) < 0x7f800000u;
+    float fk = __uint_as_float(mk), fv = __uint_as_float(mv);
+    if (!finite) {  // rare: the maxima of the finite entries alone
+      fk = fv = 0.f;
+      for (int i = 0; i < u.nr; ++i) {
+        for (int d = lane; d < D; d += 32) {
+          fk = fmaxf(fk, finite_abs(rows[i * D + d]));
+          fv = fmaxf(fv, finite_abs(__bfloat162float(vrows[i * D + d])));
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        fk = fmaxf(fk, __shfl_xor_sync(0xffffffffu, fk, o));
+        fv = fmaxf(fv, __shfl_xor_sync(0xffffffffu, fv, o));
+      }
+    }
     const float qmax = a.kv_type == SD_KV_INT8 ? 127.f : 448.f;
-    const float sk = fmaxf(fmaxf(mk / qmax, kKvMinScale), old_k), sv = fmaxf(fmaxf(mv / qmax, kKvMinScale), old_v);
+    const float sk = fmaxf(fmaxf(fk / qmax, kKvMinScale), old_k), sv = fmaxf(fmaxf(fv / qmax, kKvMinScale), old_v);
     if (earlier) {
       const long long at = (u.base * geo.G + g) * D, pitch = (long long)geo.G * D;
       const int n = u.lo - u.c * bs;
@@ -457,30 +517,36 @@ __device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBl
     }
     if (tid == 0) a.k_scales[u.blk] = sk, a.v_scales[u.blk] = sv;
     const float ik = 1.f / sk, iv = 1.f / sv;
+    const long long first = (u.base + (u.lo - u.c * bs)) * geo.G + g;
 #pragma unroll 2
     for (int i = tid / LANES; i < u.nr; i += RPP) {
-      const uint2 vx = *reinterpret_cast<const uint2*>(vs + i * a.v_stride);  // read before, still in L2
-      const uint2 vy = *reinterpret_cast<const uint2*>(vs + i * a.v_stride + D / 2);
+      const uint2 vx = *reinterpret_cast<const uint2*>(vrows + i * D + 4 * l);
+      const uint2 vy = *reinterpret_cast<const uint2*>(vrows + i * D + D / 2 + 4 * l);
       const float4 x = *reinterpret_cast<const float4*>(rows + i * D + 4 * l);
       const float4 y = *reinterpret_cast<const float4*>(rows + i * D + D / 2 + 4 * l);
       const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      const long long row = (u.base + (u.lo - u.c * bs) + i) * geo.G + g;
-      store_row<D>(a.k_pages, row, l, e, ik, a.kv_type);
+      const long long row = first + (long long)i * geo.G;
       float v[8];
       unpack_row<D>(vx, vy, v);
-      store_row<D>(a.v_pages, row, l, v, iv, a.kv_type);
+      if (finite) {
+        store_row<D, true>(a.k_pages, row, l, e, ik, a.kv_type);
+        store_row<D, true>(a.v_pages, row, l, v, iv, a.kv_type);
+      } else {
+        store_row<D>(a.k_pages, row, l, e, ik, a.kv_type);
+        store_row<D>(a.v_pages, row, l, v, iv, a.kv_type);
+      }
     }
   }
-  if (a.bounds != nullptr && tid < 2 * D) {
-    const int which = tid / D, d = tid % D;
-    __nv_bfloat16* at = a.bounds + (u.blk * 2 + which) * D + d;
-    float x = sm.bounds[which][0][d];
-    for (int i = 1; i < kKvThreads / 32; ++i) x = which ? fmaxf(x, sm.bounds[1][i][d]) : fminf(x, sm.bounds[0][i][d]);
-    if (earlier) {
-      const float old = __bfloat162float(*at);
-      x = which ? fmaxf(x, old) : fminf(x, old);
+  if (a.bounds != nullptr && tid < D) {  // two dims of one bound each
+    const int which = tid / (D / 2), d = 2 * (tid % (D / 2));
+    __nv_bfloat162* at = reinterpret_cast<__nv_bfloat162*>(a.bounds + (u.blk * 2 + which) * D + d);
+    __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&sm.bounds[which][0][d]);
+    for (int i = 1; i < kKvThreads / 32; ++i) {
+      const __nv_bfloat162 o = *reinterpret_cast<const __nv_bfloat162*>(&sm.bounds[which][i][d]);
+      x = which ? __hmax2(x, o) : __hmin2(x, o);
     }
-    *at = __float2bfloat16_rn(x);
+    if (earlier) x = which ? __hmax2(x, *at) : __hmin2(x, *at);
+    *at = x;
   }
 }
 
@@ -561,11 +627,11 @@ __device__ void store_unit_warp(const KvStoreArgs& a, const KvUnit& u, int g, ui
 // Units by row: warp w of the CTA takes (row, KV head) pair w, if the row is
 // the first new one of its block.
 template <int D, bool FULL>
-__device__ void store_by_row(const KvStoreArgs& a, KvBlockSmem<D>& sm, float* rows) {
+__device__ void store_by_row(const KvStoreArgs& a, int cta, KvBlockSmem<D>& sm, float* rows, __nv_bfloat16* vrows) {
   constexpr int LANES = D / 8, kWarps = kKvThreads / 32;
   const KvGeom& geo = a.geo;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES;
-  const int item = blockIdx.x * kWarps + warp, row = item / geo.G, g = item - row * geo.G;
+  const int item = cta * kWarps + warp, row = item / geo.G, g = item - row * geo.G;
   KvUnit u;
   u.ok = false, u.nr = 0;
   uint2 x = make_uint2(0u, 0u), y = x;
@@ -581,7 +647,7 @@ __device__ void store_by_row(const KvStoreArgs& a, KvBlockSmem<D>& sm, float* ro
       const int p = row_position(a, b, row, &r0, &p0, &p1);
       if (p >= 0 && p < p1) {
         const int c = geo.bs_div.div(p);
-        if (p == c * geo.bs || row == r0) u = make_unit(a, b, c, r0, p0, p1, g, lane == 0);
+        if (p == c * geo.bs || row == r0) u = make_unit(a, b, c, r0, p0, p1, g, lane == 0, [](int, int) {});
       }
     }
   }
@@ -593,7 +659,9 @@ __device__ void store_by_row(const KvStoreArgs& a, KvBlockSmem<D>& sm, float* ro
   for (int w = 0; w < kWarps; ++w) {
     const KvUnit v = sm.units[w];
     if (!v.ok || v.nr <= 1) continue;
-    store_unit_cta<D, FULL>(a, v, (blockIdx.x * kWarps + w) % geo.G, sm, rows);
+    const int gw = (cta * kWarps + w) % geo.G;
+    copy_unit_rows<D>(a, v.row0, v.nr, gw, rows, vrows);
+    store_unit_cta<D, FULL>(a, v, gw, sm, rows, vrows);
     __syncthreads();  // its shared memory is free again
   }
 }
@@ -601,10 +669,10 @@ __device__ void store_by_row(const KvStoreArgs& a, KvBlockSmem<D>& sm, float* ro
 // Units by touched block: unit u of the list over all requests, one CTA per
 // KV head.
 template <int D, bool FULL>
-__device__ void store_by_block(const KvStoreArgs& a, KvBlockSmem<D>& sm, float* rows) {
+__device__ void store_by_block(const KvStoreArgs& a, int cta, KvBlockSmem<D>& sm, float* rows, __nv_bfloat16* vrows) {
   const KvGeom& geo = a.geo;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int unit = blockIdx.x / geo.G, g = blockIdx.x % geo.G;
+  const int unit = cta / geo.G, g = cta % geo.G;
   int r0, p0, p1;
   if (tid == 0) sm.unit[0] = -1;
   int before = 0;
@@ -638,8 +706,10 @@ __device__ void store_by_block(const KvStoreArgs& a, KvBlockSmem<D>& sm, float* 
   if (sm.unit[0] < 0) return;
   const int b = sm.unit[0];
   row_position(a, b, 0, &r0, &p0, &p1);
-  const KvUnit u = make_unit(a, b, geo.bs_div.div(max(p0, 0)) + sm.unit[1], r0, p0, p1, g, tid == 0);
-  if (u.ok) store_unit_cta<D, FULL>(a, u, g, sm, rows);
+  const KvUnit u = make_unit(a, b, geo.bs_div.div(max(p0, 0)) + sm.unit[1], r0, p0, p1, g, tid == 0,
+                             [&](int row0, int nr) { copy_unit_rows<D>(a, row0, nr, g, rows, vrows); });
+  if (u.ok) store_unit_cta<D, FULL>(a, u, g, sm, rows, vrows);
+  else cp_async_wait<0>();
 }
 
 template <int D, bool FULL>
@@ -649,9 +719,15 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv_store_kernel(const __grid_co
   pdl_wait();  // inputs come from earlier work in the stream
   pdl_trigger();
   float* rows = reinterpret_cast<float*>(smem_raw);
-  if (blockIdx.x >= a.kv_ctas) store_queries<D, FULL>(a);
-  else if (a.by_row) store_by_row<D, FULL>(a, sm, rows);
-  else store_by_block<D, FULL>(a, sm, rows);
+  __nv_bfloat16* vrows = reinterpret_cast<__nv_bfloat16*>(rows + a.geo.bs * D);
+  // CTAs of both kinds evenly mixed: K and V are bound by issue slots and
+  // latency, q by HBM
+  const unsigned int all = a.kv_ctas + a.q_ctas;
+  const int before = static_cast<int>((unsigned long long)blockIdx.x * a.q_ctas / all);
+  const int cta = blockIdx.x - before;
+  if (static_cast<int>((blockIdx.x + 1ull) * a.q_ctas / all) > before) store_queries<D, FULL>(a, before);
+  else if (a.by_row) store_by_row<D, FULL>(a, cta, sm, rows, vrows);
+  else store_by_block<D, FULL>(a, cta, sm, rows, vrows);
 }
 
 // Reads the tokens that a store with the same tok_start and seqlens wrote back

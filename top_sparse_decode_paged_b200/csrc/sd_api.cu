@@ -1239,10 +1239,11 @@ sd_status sd_kv_store(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
     return SD_ERR_UNSUPPORTED;
   if (B == 0 || n_tokens == 0) return SD_OK;
   a.kv_ctas = static_cast<int>(kv_ctas);
+  a.q_ctas = static_cast<int>(q_ctas);
   auto kern = kv.D == 64 ? (full ? sd::kv_store_kernel<64, true> : sd::kv_store_kernel<64, false>)
                          : (full ? sd::kv_store_kernel<128, true> : sd::kv_store_kernel<128, false>);
-  // the rotated K of a block between its two passes (8-bit pools)
-  const size_t smem = kv.kv_type == SD_KV_BF16 ? 0 : (size_t)kv.block_tokens * kv.D * sizeof(float);
+  // a block's new rows: K in fp32, V in bf16
+  const size_t smem = (size_t)kv.block_tokens * kv.D * (sizeof(float) + sizeof(uint16_t));
   if (smem > 32 * 1024 && (s = set_smem_limit(reinterpret_cast<const void*>(kern), smem)) != SD_OK) return s;
   return launch_k(kern, dim3(static_cast<unsigned>(kv_ctas + q_ctas)), dim3(sd::kKvThreads), smem,
                   static_cast<cudaStream_t>(stream), a);
