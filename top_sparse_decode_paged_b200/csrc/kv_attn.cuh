@@ -269,6 +269,7 @@ __device__ __forceinline__ int warp_inclusive_sum(int x) {
 // Tiles of requests [0, end), by one warp.
 __device__ __forceinline__ int kv_attn_sum(const KvAttnArgs& a, int end) {
   int n = 0;
+#pragma unroll 1
   for (int b = threadIdx.x & 31; b < end; b += 32) n += kv_attn_tiles(a, b);
   return __reduce_add_sync(0xffffffffu, n);
 }
@@ -278,6 +279,7 @@ __device__ __forceinline__ int kv_attn_sum(const KvAttnArgs& a, int end) {
 __device__ __forceinline__ int kv_attn_find(const KvAttnArgs& a, int t, int cnt, int incl, int* first) {
   const int lane = threadIdx.x & 31;
   int before = 0;
+#pragma unroll 1
   for (int base = 0;; base += 32) {
     if (base > 0) {
       cnt = base + lane < a.B ? kv_attn_tiles(a, base + lane) : 0;
@@ -349,6 +351,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
     }
     if ((++ptile) * a.spw * kKaTile >= plen) {  // next request that has tiles
       ptile = 0;
+#pragma unroll 1
       do {
         ++pb;
         if (pb >= a.B) {
@@ -589,6 +592,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
   }
   begin_request();
   int stage = 0;
+#pragma unroll 1
   for (int at = 0; at < my; ++at) {
     cp_async_wait<C::kStages - 2>();
     __syncwarp();
@@ -746,6 +750,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
       const int done = cb;
       if (at + 1 < my) {
         ctile = 0;
+#pragma unroll 1
         do clen = kv_attn_len(a, ++cb);
         while (clen == 0 && cb + 1 < a.B);
         fetch_q(cb);
@@ -810,6 +815,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_attn_combine_kerne
     acc.x = f1 * acc.x + f2 * x.x, acc.y = f1 * acc.y + f2 * x.y;
     acc.z = f1 * acc.z + f2 * x.z, acc.w = f1 * acc.w + f2 * x.w;
   };
+#pragma unroll 1
   for (int i0 = grp; i0 < parts; i0 += GROUPS * BATCH) {
     float2 ml[BATCH];
     float4 x[BATCH];
@@ -839,7 +845,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_attn_combine_kerne
   if (lane == 0) s_ml[warp] = make_float2(M, l);
   __syncthreads();
   if (tid >= LANES) return;
-#pragma unroll
+#pragma unroll 1
   for (int w = 1; w < WARPS; ++w) add(s_ml[w].x, s_ml[w].y, s_o[w][tid]);
   const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: nothing was attended
   *reinterpret_cast<uint2*>(a.out + (size_t)bh * D + slice * (4 * LANES) + 4 * tid) =

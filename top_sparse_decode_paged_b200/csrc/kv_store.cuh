@@ -80,6 +80,7 @@ __device__ __forceinline__ int find_request(const int32_t* tok_start, int B, int
   if (__all_sync(0xffffffffu, tok_start[guess] <= r && r < tok_start[guess + 1])) return guess;
   const int base = (threadIdx.x & 31) & ~(LANES - 1);
   int lo = 0;
+#pragma unroll 1
   for (int span = B; span > 1;) {
     const int step = (span + LANES - 1) / LANES;
     const int i = lo + l * step;
@@ -202,7 +203,8 @@ struct Rotation {
 };
 
 // Four codes round(e * inv), any input: NaN is 0, infinities the largest code.
-__device__ __forceinline__ uint32_t encode4(const float* e, float inv, int kv_type) {
+__device__ __noinline__ uint32_t encode4_any(float e0, float e1, float e2, float e3, float inv, int kv_type) {
+  const float e[4] = {e0, e1, e2, e3};
   if (kv_type == SD_KV_INT8) {
     uint32_t w = 0;
 #pragma unroll
@@ -221,6 +223,10 @@ __device__ __forceinline__ uint32_t encode4(const float* e, float inv, int kv_ty
   const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(z[0], z[1]), __NV_SATFINITE, __NV_E4M3);
   const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(z[2], z[3]), __NV_SATFINITE, __NV_E4M3);
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+__device__ __forceinline__ uint32_t encode4(const float* e, float inv, int kv_type) {
+  return encode4_any(e[0], e[1], e[2], e[3], inv, kv_type);
 }
 
 // The same for finite e with |e * inv| <= 127 in int8: adding 1.5 * 2^23
@@ -256,7 +262,7 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 // Codes of rows [0, n), `pitch` bytes apart, scaled by ratio < 1, by `threads`
 // threads of which this is number `i0`.
-__device__ __forceinline__ void recode_rows(uint8_t* first, long long pitch, int n, int D, float ratio, int kv_type, int i0,
+__device__ __noinline__ void recode_rows(uint8_t* first, long long pitch, int n, int D, float ratio, int kv_type, int i0,
                                             int threads) {
   const int per_row = D / 16;
 #pragma unroll 2
@@ -268,7 +274,7 @@ __device__ __forceinline__ void recode_rows(uint8_t* first, long long pitch, int
     for (int j = 0; j < 4; ++j) {
       float e[4];
       decode4(u[j], kv_type, e);
-      u[j] = encode4(e, ratio, kv_type);
+      u[j] = encode4_finite(e, ratio, kv_type);
     }
     *at = w;
   }
@@ -323,6 +329,7 @@ __device__ void store_queries(const KvStoreArgs& a, int cta) {
   const __nv_bfloat16* src = a.q + token * a.q_stride + 4 * l;
   __nv_bfloat16* dst = a.q_out + (long long)token * a.H * D;
   // the loop bound is the same for every group of a warp (shuffles inside)
+#pragma unroll 1
   for (int i = 0; i < a.heads_per_group; i += kKvQHeads) {
     uint2 x[kKvQHeads], y[kKvQHeads];
 #pragma unroll
@@ -404,7 +411,7 @@ __device__ __forceinline__ void copy_unit_rows(const KvStoreArgs& a, int row0, i
   const int l = threadIdx.x % LANES;
   const __nv_bfloat16* ks = a.k + row0 * a.k_stride + (long long)g * D + 4 * l;
   const __nv_bfloat16* vs = a.v + row0 * a.v_stride + (long long)g * D + 4 * l;
-#pragma unroll 2
+#pragma unroll 1
   for (int i = threadIdx.x / LANES; i < nr; i += RPP) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -509,7 +516,9 @@ __device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBl
     float fk = __uint_as_float(mk), fv = __uint_as_float(mv);
     if (!finite) {  // rare: the maxima of the finite entries alone
       fk = fv = 0.f;
+#pragma unroll 1
       for (int i = 0; i < u.nr; ++i) {
+#pragma unroll 1
         for (int d = lane; d < D; d += 32) {
           fk = fmaxf(fk, finite_abs(rows[i * D + d]));
           fv = fmaxf(fv, finite_abs(__bfloat162float(vrows[i * D + d])));
@@ -532,7 +541,7 @@ __device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBl
     if (tid == 0) a.k_scales[u.blk] = sk, a.v_scales[u.blk] = sv;
     const float ik = 1.f / sk, iv = 1.f / sv;
     const long long first = (u.base + (u.lo - u.c * bs)) * geo.G + g;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = tid / LANES; i < u.nr; i += RPP) {
       const uint2 vx = *reinterpret_cast<const uint2*>(vrows + i * D + 4 * l);
       const uint2 vy = *reinterpret_cast<const uint2*>(vrows + i * D + D / 2 + 4 * l);
@@ -555,6 +564,7 @@ __device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBl
     const int which = tid / (D / 2), d = 2 * (tid % (D / 2));
     __nv_bfloat162* at = reinterpret_cast<__nv_bfloat162*>(a.bounds + (u.blk * 2 + which) * D + d);
     __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&sm.bounds[which][0][d]);
+#pragma unroll 1
     for (int i = 1; i < kKvThreads / 32; ++i) {
       const __nv_bfloat162 o = *reinterpret_cast<const __nv_bfloat162*>(&sm.bounds[which][i][d]);
       x = which ? __hmax2(x, o) : __hmin2(x, o);
@@ -670,6 +680,7 @@ __device__ void store_by_row(const KvStoreArgs& a, int cta, KvBlockSmem<D>& sm, 
   const bool many = u.ok && u.nr > 1;
   if (lane == 0) sm.units[warp] = u;
   if (!__syncthreads_or(many)) return;
+#pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
     const KvUnit v = sm.units[w];
     if (!v.ok || v.nr <= 1) continue;
@@ -690,6 +701,7 @@ __device__ void store_by_block(const KvStoreArgs& a, int cta, KvBlockSmem<D>& sm
   int r0, p0, p1;
   if (tid == 0) sm.unit[0] = -1;
   int before = 0;
+#pragma unroll 1
   for (int base = 0; base < a.B; base += kKvThreads) {
     const int i = base + tid;
     int n = 0;
@@ -707,6 +719,7 @@ __device__ void store_by_block(const KvStoreArgs& a, int cta, KvBlockSmem<D>& sm
     if (lane == 31) sm.scan[warp] = incl;
     __syncthreads();
     int skip = before, all = 0;
+#pragma unroll 1
     for (int w = 0; w < kKvThreads / 32; ++w) {
       skip += w < warp ? sm.scan[w] : 0;
       all += sm.scan[w];
@@ -783,6 +796,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(const __grid_consta
   }
   const int per_head = a.D / 16, n = geo.G * per_head;
   constexpr int kBatch = 4;  // pieces a lane has in flight
+#pragma unroll 1
   for (int i0 = lane; i0 < 2 * n; i0 += 32 * kBatch) {
     uint4 w[kBatch][2];
     float s[kBatch];

@@ -1124,13 +1124,38 @@ sd_status check_block_topk_args(const uint16_t* q, const sd_kv_cache& kv, const 
 }
 
 template <int D>
-sd_status launch_block_score(sd::BlockScoreArgs& a, cudaStream_t st) {
-  // blocks per warp: as many as leave two warps per scheduler
-  a.chunk = sd::kBtChunk;
-  const long long blocks = (long long)a.B * a.geo.G * a.max_blocks;
-  while (a.chunk > 8 && blocks < 148ll * 8 * a.chunk) a.chunk /= 2;
-  const dim3 grid(std::max(1, sd::ceil_div(a.max_blocks, a.chunk * sd::kBtWarps)), a.B * a.geo.G);
+sd_status launch_block_score(const sd::BlockScoreArgs& a, cudaStream_t st) {
+  const dim3 grid(std::max(1, sd::ceil_div(a.max_blocks, sd::kBtChunk * (sd::kBtThreads / 32))), a.B * a.geo.G);
   return launch_k(sd::block_score_kernel<D>, grid, dim3(sd::kBtThreads), 0, st, a);
+}
+
+// Scores and selection of rows of up to kBsMaxBlocks blocks in one launch, a
+// cluster per row: as many CTAs as one wave holds (two per SM), at least 32
+// blocks each.
+template <int D>
+sd_status launch_block_select(const sd::BlockScoreArgs& a, int n, int32_t* indices, cudaStream_t st) {
+  auto kern = sd::block_topk_kernel<D>;
+  const sd_status s = set_smem_limit(reinterpret_cast<const void*>(kern), sd::kBsSmem);
+  if (s != SD_OK) return s;
+  const int rows = a.B * a.geo.G;
+  int cs = 1;
+  while (cs < 8 && (long long)rows * 2 * cs <= 2 * 148 && a.max_blocks > 32 * cs) cs *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cs, rows, 1);
+  cfg.blockDim = dim3(sd::kBsThreads, 1, 1);
+  cfg.dynamicSmemBytes = sd::kBsSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = t_stage_count == 0 ? 2 : 1;  // see launch_k
+  ++t_launches;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kern, a, n, indices));
 }
 
 sd_status launch_block_topk(const uint16_t* q, const sd_kv_cache& kv, const int32_t* bt, const int32_t* seqlens,
@@ -1154,17 +1179,12 @@ sd_status launch_block_topk(const uint16_t* q, const sd_kv_cache& kv, const int3
   a.keys = static_cast<int32_t*>(ws);
   a.counts = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + block_keys_bytes(B, G, max_blocks));
   stage_mark(kStageIndexer, 0, st);
-  const sd_status s = kv.D == 64 ? launch_block_score<64>(a, st) : launch_block_score<128>(a, st);
+  const bool one = max_blocks <= sd::kBsMaxBlocks;
+  const sd_status s = one ? (kv.D == 64 ? launch_block_select<64>(a, n_select, indices, st) : launch_block_select<128>(a, n_select, indices, st))
+                          : (kv.D == 64 ? launch_block_score<64>(a, st) : launch_block_score<128>(a, st));
   stage_mark(kStageIndexer, 1, st);
-  if (s != SD_OK) return s;
-  if (max_blocks > sd::kBsMaxBlocks)
-    return launch_topk(a.keys, a.counts, indices, B, G, max_blocks, max_blocks, n_select, sd::RowMap{}, nullptr, st);
-  stage_mark(kStageTopk, 0, st);
-  const sd_status s2 = launch_k(sd::block_select_kernel, dim3(B * G), dim3(sd::kBsThreads), 0, st,
-                                static_cast<const int32_t*>(a.keys), static_cast<const int32_t*>(a.counts), G,
-                                std::max(max_blocks, 1), n_select, indices);
-  stage_mark(kStageTopk, 1, st);
-  return s2;
+  if (s != SD_OK || one) return s;
+  return launch_topk(a.keys, a.counts, indices, B, G, max_blocks, max_blocks, n_select, sd::RowMap{}, nullptr, st);
 }
 
 }  // namespace
