@@ -391,6 +391,9 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
   auto k_swizzle = [](int k) { return D == 128 ? (k & 1) | ((k >> 2) & 3) << 1 : (k >> 2) & 3; };
   auto v_swizzle = [](int k) { return D == 128 ? k & 7 : (k >> 1) & 3; };
   const uint32_t ring_at = smem_u32(ring);
+  // the cache is streamed past L2's other contents: partials, code
+  uint64_t once;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
   const uint8_t* k_src = a.k_pages + cpiece * 16;
   const uint8_t* v_src = a.v_pages + cpiece * 16;
   auto issue = [&](int stage) {
@@ -420,8 +423,8 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
       const uint32_t v_at = base + C::kRowBytes + k * D + ((cpiece ^ v_swizzle(k)) << 4);
       if (whole) {
         const size_t at = (size_t)row * 16;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(k_at), "l"(k_src + at) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(v_at), "l"(v_src + at) : "memory");
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;\n" ::"r"(k_at), "l"(k_src + at), "l"(once) : "memory");
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;\n" ::"r"(v_at), "l"(v_src + at), "l"(once) : "memory");
       } else {  // rows without a token are filled with zeros
         const int bytes = row != ~0u ? 16 : 0;
         const size_t at = row != ~0u ? (size_t)row * 16 : 0;
