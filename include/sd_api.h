@@ -320,8 +320,8 @@ sd_status sd_indexer_topk_noalloc(const int8_t* qi, const int32_t* w, const int8
  * k_bounds holds the smallest and the largest key of every block, KV head and
  * dim, for the selection of blocks; it may be NULL where nothing is selected.
  * Its entries, like the scales, stand for the tokens that the block holds.
- * D in {64, 128}, block_tokens <= 128, num_pages * page_size and
- * max_pages_per_req * page_size < 2^31; pools and bounds 16-byte aligned
+ * D in {64, 128}, block_tokens <= 128, num_pages * page_size < 2^31 and
+ * max_pages_per_req * page_size < 2^30; pools and bounds 16-byte aligned
  * (SD_ERR_INVALID_ARG otherwise). (No counterpart on the pages: they read
  * caches that a serving stack has written.) */
 typedef enum sd_kv_type { SD_KV_BF16 = 0, SD_KV_INT8 = 1, SD_KV_E4M3 = 2 } sd_kv_type;
@@ -397,7 +397,7 @@ sd_status sd_kv_load(sd_kv_cache kv, const int32_t* tok_start, const int32_t* bl
  *   out      bf16 [B, H, D], 8-byte aligned; zero where nothing is attended
  *   lse      fp32 [B, H] or NULL: ln sum exp z, -inf where nothing is attended
  * H % G == 0, H / G <= 128, n_list * index_block < 2^30, pools below 64 GiB. Scales must be finite
- * and not negative. A token on a bad page is skipped and flags SD_DEVERR_PAGE.
+ * and not negative (a V scale below 2^-100 counts as 2^-100). A token on a bad page is skipped and flags SD_DEVERR_PAGE.
  * Slots behind a request's last token may hold anything.
  * kv_type SD_KV_BF16 returns SD_ERR_UNSUPPORTED (sd_sparse_attn reads bf16 pools).
  * Workspace: sd_kv_attn_workspace_size(). */

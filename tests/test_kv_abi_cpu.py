@@ -50,7 +50,7 @@ def test_every_call_checks_the_cache(lib, over, status):
 
 def test_geometry(lib):
     for pd, status in ((api.PagedDesc(0, 32, 4, 2), INVALID), (api.PagedDesc(8, 32, 4, 0), INVALID),
-                       (api.PagedDesc(1 << 27, 32, 4, 2), UNSUPPORTED), (api.PagedDesc(8, 32, 1 << 27, 2), UNSUPPORTED)):
+                       (api.PagedDesc(1 << 27, 32, 4, 2), UNSUPPORTED), (api.PagedDesc(8, 32, 1 << 25, 2), UNSUPPORTED)):
         assert _store(lib, pd=pd) == status
     assert _store(lib, _kv(bs=256), pd=api.PagedDesc(8, 256, 4, 2)) == UNSUPPORTED  # blocks of at most 128 slots
 

@@ -101,6 +101,76 @@ def test_dominant_token_with_a_tiny_value_scale():
     assert_attention(out, lse, ref, 64)
 
 
+def test_blocks_of_zero_values():
+    """A block whose V is zero, with a scale of zero or the store's smallest:
+    its tokens keep their softmax weight."""
+    import torch
+    import top_sparse_decode_paged_b200 as sd
+    for kind in ("int8", "e4m3"):
+        for scale in (0.0, 2.0 ** -100):
+            cache, t, view = random_cache(kind, [64], 16, 16, 1, 64, seed=22, spread=0.0)
+            q = bf16_normal((1, 3, 64), 23, 2.0)
+            page = int(t[0, 1])
+            cache.v_pages.view(torch.uint8)[page] = 0
+            cache.v_scales[page] = scale
+            view["v"][page], view["vs"][page] = 0, scale
+            lse = torch.empty((1, 3), device="cuda")
+            out = sd.sd_kv_attn(q.cuda(), cache, torch.from_numpy(t).cuda(), torch.tensor([64], dtype=torch.int32).cuda(), 0.5, lse=lse)
+            assert_attention(out, lse, oracle.attend(f64(q), view, t, 16, [64], 0.5), 64)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_a_warp_that_walks_many_tiles(kind):
+    """So many KV heads that one CTA takes a whole request of more than 1024
+    tiles per warp: integer sums are folded before they can overflow. Values and
+    weights are all near their largest."""
+    import torch
+    import top_sparse_decode_paged_b200 as sd
+    G, D, P, L = 1184, 64, 64, 36000
+    N = -(-L // P)
+    g = torch.Generator(device="cuda").manual_seed(24)
+    dt = torch.int8 if kind == "int8" else torch.float8_e4m3fn
+    make = lambda lo, hi: torch.randint(lo, hi, (N, P, G, D), generator=g, device="cuda", dtype=torch.uint8).view(dt)  # noqa: E731
+    k, v = make(0, 40), make(120, 127)  # e4m3: 0x78 .. 0x7e are 256 .. 448
+    ks = torch.full((N, 1, G), 1e-3, device="cuda")
+    vs = torch.full((N, 1, G), 0.01, device="cuda")
+    cache = sd.KvCache(k, v, ks, vs)
+    q = bf16_normal((1, G, D), 25).cuda()
+    table = torch.randperm(N, generator=g, device="cuda").to(torch.int32)[None].contiguous()
+    lse = torch.empty((1, G), device="cuda")
+    out = sd.sd_kv_attn(q, cache, table, torch.tensor([L], dtype=torch.int32).cuda(), 0.125, lse=lse)
+    for h in (0, 7, 8, 500, G - 1):
+        row = table[0].long().repeat_interleave(P)[:L] * P + torch.arange(L, device="cuda") % P
+        kk = k.view(N * P, G, D)[row, h].double() * 1e-3
+        vv = v.view(N * P, G, D)[row, h].double() * float(vs[0, 0, 0])
+        z = 0.125 * (kk @ q[0, h].double())
+        ref = torch.softmax(z, 0) @ vv
+        # the output's rounding, 2^-8; codes and weights are of one sign, so
+        # every other error stays below 2^-10 of the value
+        assert ((out[0, h].double() - ref).abs() <= 2.0 ** -8 * (1 + 2.0 ** -2) * ref.abs()).all()
+        assert abs(float(lse[0, h]) - float(torch.logsumexp(z, 0))) < 1e-4
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace."""
+    import torch
+    import top_sparse_decode_paged_b200 as sd
+    lens = [5000] * 8
+    cache, t, _ = random_cache("int8", lens, 32, 32, 2, 64, seed=26)
+    tt, ln = torch.from_numpy(t).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    qs = [bf16_normal((8, 8, 64), 27 + i).cuda() for i in range(2)]
+    want = [sd.sd_kv_attn(q, cache, tt, ln, 0.1) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [sd.alloc_kv_attn_workspace(8, 2, 8, 64) for _ in range(2)]
+    outs = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, s, w, o in zip(qs, streams, ws, outs):
+            sd.sd_kv_attn(q, cache, tt, ln, 0.1, out=o, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
 def test_zero_query_and_a_query_that_is_not_finite():
     import torch
     import top_sparse_decode_paged_b200 as sd

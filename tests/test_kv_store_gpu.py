@@ -294,6 +294,40 @@ def test_bad_page_and_more_rows_than_the_request_holds():
     assert (out[0][16:25] == 0).all()
 
 
+def test_single_tokens_among_chunks():
+    """Mixed batches: requests with one new token among some with a few, and
+    one long prompt among single tokens."""
+    for new in ([1, 1, 5, 1, 0, 2, 1, 1], [1, 1, 1, 90, 1, 1, 1], [3] * 20):
+        old = [7 * i % 23 for i in range(len(new))]
+        lens = [a + b for a, b in zip(old, new)]
+        c = Loop("int8", lens, 32, 16, 3, 128, 2, seed=len(new))
+        c.store(np.concatenate([[0], np.cumsum(old)]), old, 80)
+        c.store(np.concatenate([[0], np.cumsum(new)]), lens, 81, pad=3)
+
+
+def test_starts_out_of_order_touch_nothing_outside():
+    """tok_start that is not ascending is the caller's error: flagged or
+    ignored, and no row of another request's blocks changes hands outside the pools."""
+    import torch
+    import top_sparse_decode_paged_b200 as sd
+    cache = sd.alloc_kv_cache(6, 16, 1, 64, torch.int8, 16)
+    bt = torch.arange(6, dtype=torch.int32).cuda().view(3, 2)
+    ln = torch.tensor([20, 3, 32], dtype=torch.int32).cuda()
+    k = bf16_normal((40, 1, 64), 1).cuda()
+    for ts in ([0, 30, 10, 40], [0, -5, 20, 40], [5, 5, 5, 5], [40, 20, 10, 0], [0, 1000000, 3, 40]):
+        t = torch.tensor(ts, dtype=torch.int32).cuda()
+        sd.sd_kv_store(None, k, k, cache, bt, ln, t, None)
+        sd.sd_kv_load(cache, bt, ln, t, 40)
+    sd.device_errors(clear=True)
+    t = torch.tensor([0, 20, 23, 40], dtype=torch.int32).cuda()
+    sd.sd_kv_store(None, k, k, cache, bt, ln, t, None)
+    got = f64(sd.sd_kv_load(cache, bt, ln, t, 40)[0])
+    assert sd.device_errors() == 0
+    ref = f64(k)
+    # codes may have been coded anew under a scale of the calls above: one more half step
+    assert (np.abs(got - ref) <= 2 * np.abs(ref).max() / 254 + 2.0 ** -8 * np.abs(ref)).all()
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 def test_a_serving_loop(kind):
     """Prompts, then decode steps with selected blocks, as a server runs them:

@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int k = tk + 2 * (r & 1) + 16 * (r >> 1), x = 2 * (r & 1);
-      const float ks = sc[k], vs = fmaxf(sc[kKaTile + k], FLT_MIN);
+      const float ks = sc[k], vs = fmaxf(sc[kKaTile + k], kKvMinScale);
       const float lv = fast_log2(vs);
       isv[r] = __fdividef(1.f, vs);
 #pragma unroll

@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_load_kernel(const __grid_consta
   const int p = L - (a.tok_start[b + 1] - token);
   const KvGeom& geo = a.geo;
   long long row = -1, blk = 0;
-  if (p < 0) {
+  if (p < 0 || p >= L) {
     raise_error(SD_DEVERR_INDEX);
   } else {
     const int pi = geo.page_div.div(p);

@@ -981,7 +981,7 @@ sd_status check_cache(const sd_kv_cache& kv, const sd_paged_desc& pd) {
       !aligned(kv.v_scales, 4))
     return SD_ERR_INVALID_ARG;
   if ((kv.D != 64 && kv.D != 128) || kv.block_tokens > sd::kKvMaxBlock) return SD_ERR_UNSUPPORTED;
-  if ((long long)pd.num_pages * pd.page_size >= (1ll << 31) || (long long)pd.max_pages_per_req * pd.page_size >= (1ll << 31))
+  if ((long long)pd.num_pages * pd.page_size >= (1ll << 31) || (long long)pd.max_pages_per_req * pd.page_size >= (1ll << 30))
     return SD_ERR_UNSUPPORTED;
   return SD_OK;
 }
