@@ -410,7 +410,8 @@ sd_status sd_kv_attn(const uint16_t* q, sd_kv_cache kv, const int32_t* block_tab
 /* Selection of blocks by a bound on their scores (any kv_type; kv.k_bounds is
  * read, the pools are not): block c of KV head g scores
  *   max over the group's query heads of sum_d max(q_d * lo_d, q_d * hi_d)
- * summed in fp64 and rounded to fp32, at least the largest q . k of the block.
+ * summed in fp64 and rounded to fp32, at least the largest q . k of the block
+ * (a head whose sum is not a number is left out; the bounds are finite).
  *   q        bf16 [B, H, D], 8-byte aligned
  *   indices  int32 [B, G, n_select]  OUT: the first n_first and the last n_last
  *            blocks of the request and the best others, min(n_select, number

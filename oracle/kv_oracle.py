@@ -79,12 +79,14 @@ def attend(q, cache, block_table, P, seqlens, scale, picked=None, index_block=1)
 
 
 def block_scores(q, bounds, block_table, P, bs, b, g, per, count):
-    """fp32 roundings of the bounds of request b's blocks under KV head g."""
+    """fp32 roundings of the bounds of request b's blocks under KV head g; a
+    head whose sum is not a number (infinities of both signs) is left out."""
     s = np.empty(count, dtype=np.float32)
     for c in range(count):
         page, slot = token_slot(block_table, P, b, c * bs)
         lo, hi = bounds[page, slot // bs, g]
-        s[c] = np.float32(max(np.maximum(q[b, h] * lo, q[b, h] * hi).sum() for h in range(g * per, (g + 1) * per)))
+        sums = [np.maximum(q[b, h] * lo, q[b, h] * hi).sum() for h in range(g * per, (g + 1) * per)]
+        s[c] = np.float32(max(-np.inf if np.isnan(x) else x for x in sums))
     return s
 
 

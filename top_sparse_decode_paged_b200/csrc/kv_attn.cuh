@@ -148,12 +148,6 @@ __device__ __forceinline__ void mma_8bit_16832(uint32_t* d, const uint32_t* a, u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 }
-__device__ __forceinline__ void ldmatrix_x4_at(uint32_t* r, uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(at)
-               : "memory");
-}
 // Two 16 x 16 byte matrices, transposed: lane (n, t) gets bytes 4t .. 4t + 3 of
 // columns n (r[0], r[2]) and n + 8 (r[1], r[3]).
 __device__ __forceinline__ void ldmatrix_bytes_trans_x2(uint32_t* r, uint32_t at) {
