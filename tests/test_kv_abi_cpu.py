@@ -84,6 +84,10 @@ def test_attention_arguments(lib):
         assert _attn(lib, **bad) == INVALID, bad
     for bad in (dict(kv=_kv(kind=0)), dict(H=512), dict(idx=256, n=1 << 20, ib=1 << 10), dict(B=1 << 30, H=4)):
         assert _attn(lib, **bad) == UNSUPPORTED, bad
+    # 2^36 tokens over all requests, in the table or in listed blocks, are too many; half as many are not
+    for walk in (dict(pd=api.PagedDesc(8, 32, 1 << 24, 2)), dict(idx=256, n=1, ib=1 << 29), dict(idx=256, n=1 << 20, ib=512, pd=api.PagedDesc(8, 32, 1 << 24, 2))):
+        assert _attn(lib, B=128, **walk) == UNSUPPORTED, walk
+        assert _attn(lib, B=64, **walk) == WORKSPACE, walk
     need = lib.sd_kv_attn_workspace_size(1, 2, 4, 64)
     assert need > 0 and need % 256 == 0
     assert _attn(lib) == WORKSPACE

@@ -1019,16 +1019,21 @@ KvAttnPlan kv_attn_plan(int B, int G, int H, int D) {
 }
 
 sd_status check_kv_attn_args(const uint16_t* q, const sd_kv_cache& kv, const int32_t* bt, const int32_t* seqlens,
-                             const sd_paged_desc& pd, int B, int H, float scale, const uint16_t* out) {
+                             const sd_paged_desc& pd, int B, int H, float scale, const uint16_t* out, bool list,
+                             int n_list, int index_block) {
   const sd_status s = check_cache(kv, pd);
   if (s != SD_OK) return s;
   if (B < 0 || H <= 0 || H % pd.kv_heads != 0 || !isfinite(scale)) return SD_ERR_INVALID_ARG;
   if (B > 0 && (!q || !bt || !seqlens || !out || !aligned(q, 16) || !aligned(out, 8))) return SD_ERR_INVALID_ARG;
   // rows are addressed in 16-byte units held in 32 bits: pools up to 64 GiB
   if ((unsigned long long)pd.num_pages * pd.page_size * pd.kv_heads * kv.D >= (1ull << 36) - 16) return SD_ERR_UNSUPPORTED;
-  if (kv.kv_type == SD_KV_BF16 || H / pd.kv_heads > 128 || (long long)B * H >= (1ll << 29) ||
-      (long long)B * pd.max_pages_per_req * pd.page_size >= (1ll << 36))  // tiles are counted in 32 bits
-    return SD_ERR_UNSUPPORTED;
+  if (kv.kv_type == SD_KV_BF16 || H / pd.kv_heads > 128 || (long long)B * H >= (1ll << 29)) return SD_ERR_UNSUPPORTED;
+  if (list && (n_list <= 0 || index_block <= 0)) return SD_ERR_INVALID_ARG;
+  if (list && (long long)n_list * index_block >= (1ll << 30)) return SD_ERR_UNSUPPORTED;
+  // tiles of all requests together are counted in 32 bits; a list walks whole blocks
+  const long long cap = (long long)pd.max_pages_per_req * pd.page_size;
+  const long long most = list ? std::min((long long)n_list * index_block, cap + index_block) : cap;
+  if (B * ((most + sd::kKaTile - 1) / sd::kKaTile) >= (1ll << 31)) return SD_ERR_UNSUPPORTED;
   return SD_OK;
 }
 
@@ -1317,11 +1322,9 @@ sd_status sd_kv_attn(const uint16_t* q, sd_kv_cache kv, const int32_t* block_tab
                      int32_t H, float scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
                      void* stream) {
   t_launches = 0;
-  const sd_status s = check_kv_attn_args(q, kv, block_table, seqlens, pd, B, H, scale, out);
+  const sd_status s = check_kv_attn_args(q, kv, block_table, seqlens, pd, B, H, scale, out, indices != nullptr, n_list, index_block);
   if (s != SD_OK) return s;
   if (indices == nullptr) n_list = index_block = 1;
-  if (n_list <= 0 || index_block <= 0) return SD_ERR_INVALID_ARG;
-  if ((long long)n_list * index_block >= (1ll << 30)) return SD_ERR_UNSUPPORTED;
   if (!ws_ok(workspace, workspace_bytes, kv_attn_plan(B, pd.kv_heads, H, kv.D).total)) return SD_ERR_WORKSPACE;
   if (B == 0) return SD_OK;
   return launch_kv_attn(q, kv, block_table, seqlens, indices, n_list, index_block, pd, B, H, scale,
@@ -1363,7 +1366,7 @@ sd_status sd_kv_block_step(const uint16_t* q, sd_kv_cache kv, const int32_t* blo
   sd_status s =
       check_block_topk_args(q, kv, block_table, seqlens, pd, B, H, max_seqlen, n_select, n_first, n_last, indices);
   if (s != SD_OK) return s;
-  s = check_kv_attn_args(q, kv, block_table, seqlens, pd, B, H, scale, out);
+  s = check_kv_attn_args(q, kv, block_table, seqlens, pd, B, H, scale, out, true, n_select, kv.block_tokens);
   if (s != SD_OK) return s;
   if (!ws_ok(workspace, workspace_bytes,
              sd_kv_block_step_workspace_size(B, pd.kv_heads, H, kv.D, max_seqlen, kv.block_tokens)))
