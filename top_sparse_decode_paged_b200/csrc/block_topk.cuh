@@ -28,7 +28,8 @@
 // further than twice that from the border are settled, and the others, five
 // of 1024 for normal values, get their exact scores. Where the bound does not hold (values that are not finite,
 // or so large or small that a product leaves fp32's range) or over 256 blocks are too close, the
-// row is scored exactly.
+// row is scored exactly, by the one CTA that selects (128 rows of 1024 equal
+// blocks: 72 us a call, of 4096: 262 us).
 //
 // Split of the selection: rows of up to kBsMaxBlocks blocks are scored and
 // selected in one launch by a cluster per (request, KV head), whose CTAs send

@@ -27,8 +27,10 @@
 // warp per (token, KV head), K in one part of its lanes and V in the other,
 // and units of several rows fall back to the whole CTA. q: one group of D / 8 lanes per (token,
 // group of heads); the token's angles are computed once per group and used
-// for its heads. Bound by HBM for prompts and by launch and load latency
-// for a decode step.
+// for its heads. 32 query heads over 8 KV heads of 128: four prompts into int8
+// (212 MB of q, 40 M instructions) 62 us, bound by issue slots (65 % used) and
+// then HBM; three prompts into bf16 32.7 us; one token 3.7 us and 64 tokens
+// 4.7 us, bound by launch and load latency.
 #pragma once
 
 #include <float.h>
@@ -759,7 +761,8 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv_store_kernel(const __grid_co
 
 // Reads the tokens that a store with the same tok_start and seqlens wrote back
 // as bf16 rows [T, G, D]: code * scale, rounded once. One warp per token, a
-// 16-element piece per lane and step. Bound by HBM.
+// 16-element piece per lane and step. Bound by HBM: the four prompts' int8
+// rows in 14.6 us.
 struct KvLoadArgs {
   const void *k_pages, *v_pages;
   const float *k_scales, *v_scales;

@@ -1007,7 +1007,10 @@ struct KvAttnPlan {
 KvAttnPlan kv_attn_plan(int B, int G, int H, int D) {
   KvAttnPlan p{};
   const int qpk = H / G;
-  p.hpw = qpk <= 4 ? 4 : qpk <= 8 ? 8 : 16;  // query heads that share a warp's K and V
+  // Query heads that share a warp's K and V. 16 x 32768 tokens, 8 KV heads,
+  // int8: 4 heads each in fours 163 us, in eights 165, in sixteens (fp16
+  // P.V) 224; 16 heads each in sixteens 226, in eights (K and V read twice) 320.
+  p.hpw = qpk <= 4 ? 4 : qpk <= 8 ? 8 : 16;
   p.cols = G * sd::ceil_div(qpk, p.hpw);
   p.col_groups = sd::ceil_div(p.cols, sd::kKaWarps);
   p.spw = p.cols >= sd::kKaWarps ? 1 : sd::kKaWarps / p.cols;
@@ -1048,7 +1051,9 @@ sd_status launch_kv_attn_t(const sd::KvAttnArgs& a, cudaStream_t st) {
 
 template <int D>
 sd_status launch_kv_combine(const sd::KvAttnArgs& a, cudaStream_t st) {
-  // narrow groups while one wave holds their CTAs (four per SM)
+  // Narrow groups while one wave holds their CTAs (four per SM). The whole
+  // call with narrow and with wide groups: 32 rows 7.8 and 9.1 us, 128 rows
+  // of 4000 tokens 13.6 and 16.7, 512 rows of a ragged batch 37.0 and 29.9.
   constexpr int kSlices = D / 32;
   const int rows = a.B * a.H;
   if ((long long)rows * kSlices <= 4 * 148)
@@ -1136,7 +1141,8 @@ sd_status launch_block_score(const sd::BlockScoreArgs& a, cudaStream_t st) {
 
 // Scores and selection of rows of up to kBsMaxBlocks blocks in one launch, a
 // cluster per row: as many CTAs as one wave holds (two per SM), at least 32
-// blocks each.
+// blocks each (8 rows of 256 blocks: 8 CTAs 5.7 us, 2 CTAs 8.3, one 12.2; 128
+// rows of 1024: 2 CTAs 21.6, 4 in two waves 28.6, one 22.0).
 template <int D, bool APPROX>
 sd_status launch_block_select(const sd::BlockScoreArgs& a, int n, int32_t* indices, cudaStream_t st) {
   auto kern = sd::block_topk_kernel<D, APPROX>;
@@ -1256,12 +1262,14 @@ sd_status sd_kv_store(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
   a.interleaved = interleaved != 0;
   a.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
   // A request touches at most n / block_tokens + 2 blocks. Where that does not
-  // beat one unit per row (a decode step), rows are the units, a warp each.
+  // beat one unit per row (a decode step), rows are the units, a warp each:
+  // 64 tokens 4.7 us by rows and 9.4 by blocks, prompts 121 and 62.
   const long long touched = n_tokens / kv.block_tokens + 2ll * B;
   a.by_row = n_tokens <= touched;
   const int warps = sd::kKvThreads / 32;
   const long long kv_ctas = a.by_row ? ((long long)n_tokens * G + warps - 1) / warps : touched * G;
-  // heads per lane group: as many as leave two waves of groups
+  // Heads per lane group: as many as leave two waves of groups. Always 4: one
+  // token 3.7 us, prompts 75.0; always all: 9.0 and 62.1; so: 3.7 and 62.1.
   const int groups = sd::kKvThreads / (kv.D / 8);
   a.heads_per_group = std::max(1, std::min(a.H, 32));
   while (a.heads_per_group > sd::kKvQHeads &&
