@@ -84,13 +84,16 @@ struct KvAttnArgs {
 // logits of kHL heads for the tokens of rows n and n + 8.
 template <int D, int HPW, int TYPE>
 struct KvAttnCfg {
-  static constexpr bool kBytes = HPW <= 8;  // P.V on 8-bit instructions
-  static constexpr int kParts = TYPE == SD_KV_INT8 ? 3 : 2;
-  // HPW 4: column 2t + x of S tile j is part 2j + x of head t; else tile
-  // (hg, p) is part p of heads 8 hg .. 8 hg + 7
+  static constexpr bool kHalf = TYPE == SD_KV_E4M3;      // q . k on fp16 instructions
+  static constexpr bool kBytes = !kHalf && HPW <= 8;     // P.V on 8-bit instructions
+  static constexpr int kParts = kHalf ? 1 : 3;
+  // HPW 4: column 2t + x of S tile j is part 2j + x of head t (fp16: x = 0);
+  // else tile (hg, p) is part p of heads 8 hg .. 8 hg + 7
   static constexpr int kSTiles = HPW == 4 ? (kParts + 1) / 2 : HPW / 8 * kParts;
-  // O likewise, with the three parts of the weights; fp16: head groups
-  static constexpr int kOTiles = HPW == 4 ? 2 : HPW == 8 ? 3 : 2;
+  static constexpr int kQSteps = D / (kHalf ? 16 : 32);  // instructions along D
+  // O likewise, with the three parts of the weights; fp16: HPW 4: the weight
+  // and its rest, HPW 8: a tile of each, HPW 16: head groups
+  static constexpr int kOTiles = kHalf ? (HPW == 4 ? 1 : 2) : HPW == 4 ? 2 : HPW == 8 ? 3 : 2;
   static constexpr int kHL = HPW == 4 ? 1 : HPW / 4;
   static constexpr int kGroups = HPW == 16 ? 2 : 1;
   static constexpr int kRowBytes = kKaTile * D;                   // K (or V) of a stage
@@ -130,25 +133,18 @@ __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// m16n8k32 over 8-bit operands; d is four int32 (int8) or fp32 (e4m3) sums.
-// UNSIGNED: b holds unsigned bytes.
-template <int TYPE, bool UNSIGNED = false>
+// m16n8k32 over signed bytes; UNSIGNED: b holds unsigned ones.
+template <bool UNSIGNED = false>
 __device__ __forceinline__ void mma_8bit_16832(uint32_t* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if constexpr (TYPE == SD_KV_INT8 && UNSIGNED) {
+  if constexpr (UNSIGNED) {
     asm volatile(
         "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  } else if constexpr (TYPE == SD_KV_INT8) {
+  } else {
     asm volatile(
         "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  } else {
-    float* f = reinterpret_cast<float*>(d);
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 }
@@ -192,9 +188,10 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t*>(&r);
   } else {
-    const __half2_raw r =
-        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HI ? w >> 16 : w & 0xffffu), __NV_E4M3);
-    return static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
+    uint32_t r;
+    if constexpr (HI) asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(w));
+    else asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(r) : "r"(w));
+    return r;
   }
 }
 template <int TYPE>
@@ -202,58 +199,25 @@ __device__ __forceinline__ uint32_t bias_codes(uint32_t w) {
   return TYPE == SD_KV_INT8 ? w ^ 0x80808080u : w;
 }
 
-// The parts of four elements of q (already times the head's power of two), one
-// word per part, the most significant first.
-template <int TYPE>
-__device__ __forceinline__ void q_parts(const float* x, uint32_t* w) {
-  if constexpr (TYPE == SD_KV_INT8) {
-    // |f| <= 2^22; the bytes of f + 0x808080 are its digits in [-128, 127] plus 128
-    uint32_t f[4];
+// The three digits of four elements of q (already times the head's power of
+// two), one word per digit, the most significant first.
+__device__ __forceinline__ void q_digits(const float* x, uint32_t* w) {
+  // |f| <= 2^22; the bytes of f + 0x808080 are its digits in [-128, 127] plus 128
+  uint32_t f[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = static_cast<uint32_t>(__float2int_rn(x[j]) + 0x808080) ^ 0x808080u;
+  for (int j = 0; j < 4; ++j) f[j] = static_cast<uint32_t>(__float2int_rn(x[j]) + 0x808080) ^ 0x808080u;
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      const uint32_t sel = p == 0 ? 0x0062u : p == 1 ? 0x0051u : 0x0040u;
-      w[p] = __byte_perm(__byte_perm(f[0], f[1], sel), __byte_perm(f[2], f[3], sel), 0x5410);
-    }
-  } else {
-    uint32_t c[2][2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      c[0][j] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * j], x[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-      const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c[0][j]), __NV_E4M3)));
-      c[1][j] = __nv_cvt_float2_to_fp8x2(make_float2((x[2 * j] - y.x) * 16.f, (x[2 * j + 1] - y.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
-    }
-#pragma unroll
-    for (int p = 0; p < 2; ++p) w[p] = c[p][0] | (c[p][1] << 16);
+  for (int p = 0; p < 3; ++p) {
+    const uint32_t sel = p == 0 ? 0x0062u : p == 1 ? 0x0051u : 0x0040u;
+    w[p] = __byte_perm(__byte_perm(f[0], f[1], sel), __byte_perm(f[2], f[3], sel), 0x5410);
   }
 }
 
-// Weights w < 1.9 in three bytes, the most significant part highest: 24-bit
-// fixed point, or e4m3 roundings of 128 w, of 16 times the rest and of 16 times that rest.
-template <int TYPE>
-__device__ __forceinline__ void weight_parts(float w0, float w1, uint32_t* p0, uint32_t* p1) {
-  if constexpr (TYPE == SD_KV_INT8) {
-    *p0 = __float2uint_rn(w0 * 8388608.f);
-    *p1 = __float2uint_rn(w1 * 8388608.f);
-  } else {
-    // An e4m3 code c >= 0 has the value 2^8 * half(c << 7): a shift decodes it
-    // (the conversion instruction takes several times as long). The first rest in fp32,
-    // the second in fp16, whose 11 bits hold the 8 that the last two parts keep.
-    uint32_t c[3];
-    c[0] = __nv_cvt_float2_to_fp8x2(make_float2(w0 * 128.f, w1 * 128.f), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t y = __byte_perm(c[0], 0u, 0x4140) << 7;
-    const float2 yf = __half22float2(*reinterpret_cast<const __half2*>(&y));
-    const __half2 r = __floats2half2_rn(fmaf(yf.x, -4096.f, w0 * 2048.f), fmaf(yf.y, -4096.f, w1 * 2048.f));
-    c[1] = __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
-    const uint32_t z = __byte_perm(c[1], 0u, 0x1404), zs = (z & 0x80008000u) | ((z >> 1) & 0x3f803f80u);
-    const __half2 r2 = __hfma2(*reinterpret_cast<const __half2*>(&zs), __float2half2_rn(-4096.f), __hmul2(r, __float2half2_rn(16.f)));
-    c[2] = __nv_cvt_halfraw2_to_fp8x2(r2, __NV_SATFINITE, __NV_E4M3);
-    // c[i]: part i of w0 in byte 0, of w1 in byte 1
-    const uint32_t lo = c[2] | (c[1] << 16);
-    *p0 = __byte_perm(lo, c[0], 0x6420);  // part 2, part 1, part 0, zero
-    *p1 = __byte_perm(lo, c[0], 0x6531);
-  }
+// Weights in fp16, and 2^11 times what the rounding left.
+__device__ __forceinline__ void weight_halves(float w0, float w1, uint32_t* hi, uint32_t* lo) {
+  *hi = pack_half2(w0, w1);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(hi));
+  *lo = pack_half2((w0 - f.x) * 2048.f, (w1 - f.y) * 2048.f);
 }
 
 __device__ __forceinline__ int warp_inclusive_sum(int x) {
@@ -436,7 +400,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
 
   // ---- the compute side ----
   int cb = b_begin, ctile = tile_begin, clen = kv_attn_len(a, cb);
-  uint32_t qf[C::kSTiles][D / 32][2];
+  uint32_t qf[C::kSTiles][C::kQSteps][2];
   float qs[C::kHL];  // scale of this lane's heads (base-2 logits)
   float m[C::kHL], l[C::kHL];
   uint32_t o[C::kOTiles][D / 16][4] = {};  // int32 or fp32 sums; D / 16 tiles of 16 dims
@@ -446,18 +410,19 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
   auto lane_head = [&](int i) { return HPW == 4 ? t : (i >> 1) * 8 + 2 * t + (i & 1); };
   // sum of this lane's head i, dim 16 j + n + 8 x, in units of its weights and codes
   auto sum_of = [&](int i, int j, int x) {
-    if constexpr (!C::kBytes) {
+    if constexpr (C::kHalf && HPW == 4) {  // the rests are in units of 2^-11
+      return fmaf(__uint_as_float(o[0][j][2 * x + 1]), 1.f / 2048.f, __uint_as_float(o[0][j][2 * x]));
+    } else if constexpr (C::kHalf && HPW == 8) {
+      return fmaf(__uint_as_float(o[C::kOTiles - 1][j][2 * x + (i & 1)]), 1.f / 2048.f, __uint_as_float(o[0][j][2 * x + (i & 1)]));
+    } else if constexpr (!C::kBytes) {
       return __uint_as_float(o[i >> 1][j][2 * x + (i & 1)]);
     } else {
       const uint32_t p0 = HPW == 4 ? o[0][j][2 * x] : o[0][j][2 * x + (i & 1)];
       const uint32_t p1 = HPW == 4 ? o[0][j][2 * x + 1] : o[1][j][2 * x + (i & 1)];
       const uint32_t p2 = HPW == 4 ? o[1][j][2 * x] : o[C::kOTiles - 1][j][2 * x + (i & 1)];
-      if constexpr (TYPE == SD_KV_INT8)  // digits of 2^-23
-        return fmaf(static_cast<float>(static_cast<int>(p0)), 0.0078125f,
-                    fmaf(static_cast<float>(static_cast<int>(p1)), 0.0078125f / 256.f, static_cast<float>(static_cast<int>(p2)) * (0.0078125f / 65536.f)));
-      else
-        return fmaf(__uint_as_float(p0), 0.0078125f,
-                    fmaf(__uint_as_float(p1), 0.0078125f / 16.f, __uint_as_float(p2) * (0.0078125f / 256.f)));
+      // digits of 2^-23
+      return fmaf(static_cast<float>(static_cast<int>(p0)), 0.0078125f,
+                  fmaf(static_cast<float>(static_cast<int>(p1)), 0.0078125f / 256.f, static_cast<float>(static_cast<int>(p2)) * (0.0078125f / 65536.f)));
     }
   };
   uint32_t qraw[C::kGroups][D / 8];  // dims 16 kk + 4t .. + 3 in words 2 kk, 2 kk + 1 of head n (HPW 4: n / 2)
@@ -487,7 +452,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // up = 2^(e - floor(log2 amax)), as two factors since it can pass 2^127
       const int ex = min(max(static_cast<int>(top >> 23), 1), 254);  // biased; 0: zero or subnormal
-      const int up = (TYPE == SD_KV_INT8 ? 21 : 7) + 127 - ex;
+      const int up = (C::kHalf ? 10 : 21) + 127 - ex;
       const float f0 = __uint_as_float((uint32_t)(up / 2 + 127) << 23), f1 = __uint_as_float((uint32_t)(up - up / 2 + 127) << 23);
       // a query that is not finite makes its head's output NaN
       back_of[hg] = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : a.scale_log2 / f0 / f1;
@@ -495,11 +460,17 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
       for (int kk = 0; kk < D / 16; ++kk) {
         const float2 x = bf2(w[2 * kk]), y = bf2(w[2 * kk + 1]);
         const float e[4] = {x.x * f0 * f1, x.y * f0 * f1, y.x * f0 * f1, y.y * f0 * f1};
-        uint32_t p[C::kParts];
-        q_parts<TYPE>(e, p);
+        if constexpr (C::kHalf) {  // bf16 values fit fp16 down to 2^-27 of the largest
+          const bool live = HPW != 4 || (n & 1) == 0;
+          qf[hg][kk][0] = live ? pack_half2(e[0], e[1]) : 0u;
+          qf[hg][kk][1] = live ? pack_half2(e[2], e[3]) : 0u;
+          continue;
+        }
+        uint32_t p[3];
+        q_digits(e, p);
         if constexpr (HPW == 4) {
-          qf[0][kk / 2][kk % 2] = n & 1 ? p[1] : p[0];
-          if constexpr (C::kSTiles == 2) qf[1][kk / 2][kk % 2] = n & 1 ? 0u : p[2];
+          qf[0][kk / 2 % C::kQSteps][kk % 2] = n & 1 ? p[1] : p[0];
+          qf[C::kSTiles - 1][kk / 2][kk % 2] = n & 1 ? 0u : p[2];
         } else {
 #pragma unroll
           for (int i = 0; i < C::kParts; ++i) qf[hg * C::kParts + i][kk / 2][kk % 2] = p[i];
@@ -614,7 +585,19 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
         uint32_t f[4];
         ldmatrix_x4_at(f, k_read + off + mt * 16 * D + (((2 * j + (lane >> 4)) ^ k_sw) << 4));
 #pragma unroll
-        for (int h = 0; h < C::kSTiles; ++h) mma_8bit_16832<TYPE>(s[mt][h], f, qf[h][j][0], qf[h][j][1]);
+        for (int x = 0; x < (C::kHalf ? 2 : 1); ++x) {
+          if constexpr (C::kHalf) {  // codes 0, 1 and 2, 3 of each word are the instruction's column pairs
+            const uint32_t w0 = f[2 * x], w1 = f[2 * x + 1];
+            const uint32_t c[4] = {codes_to_half2<TYPE, 0>(w0), codes_to_half2<TYPE, 0>(w1), codes_to_half2<TYPE, 1>(w0),
+                                   codes_to_half2<TYPE, 1>(w1)};
+#pragma unroll
+            for (int h = 0; h < C::kSTiles; ++h)
+              mma_f16_16816(reinterpret_cast<float*>(s[mt][h]), c, qf[h][2 * j + x][0], qf[h][2 * j + x][1]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < C::kSTiles; ++h) mma_8bit_16832(s[mt][h], f, qf[h][j][0], qf[h][j][1]);
+          }
+        }
       }
     }
 
@@ -630,13 +613,13 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i) {
         const uint32_t(*p)[4] = s[r >> 1] + (HPW == 4 ? 0 : (i >> 1) * C::kParts);
-        const uint32_t p0 = HPW == 4 ? p[0][x] : p[0][x + (i & 1)], p1 = HPW == 4 ? p[0][x + 1] : p[1][x + (i & 1)];
+        const uint32_t p0 = HPW == 4 ? p[0][x] : p[0][x + (i & 1)];
         float z;
-        if constexpr (TYPE == SD_KV_INT8) {
-          const uint32_t p2 = HPW == 4 ? p[1][x] : p[C::kParts - 1][x + (i & 1)];
-          z = fmaf(static_cast<float>(static_cast<int>(p0) * 256 + static_cast<int>(p1)), 256.f, static_cast<float>(static_cast<int>(p2)));
+        if constexpr (C::kHalf) {
+          z = __uint_as_float(p0);
         } else {
-          z = fmaf(__uint_as_float(p1), 0.0625f, __uint_as_float(p0));
+          const uint32_t p1 = HPW == 4 ? p[0][x + 1] : p[1][x + (i & 1)], p2 = HPW == 4 ? p[1][x] : p[C::kParts - 1][x + (i & 1)];
+          z = fmaf(static_cast<float>(static_cast<int>(p0) * 256 + static_cast<int>(p1)), 256.f, static_cast<float>(static_cast<int>(p2)));
         }
         w[r][i] = ks >= 0.f ? fmaf(z, qs[i] * ks, lv) : -INFINITY;  // u
         over |= w[r][i] > m[i] + kKaSlack;
@@ -663,12 +646,10 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
             } else {
 #pragma unroll
               for (int h = 0; h < C::kOTiles; ++h) {
-                if constexpr (!C::kBytes) {
-                  if (h == i >> 1) o[h][j][2 * x + (i & 1)] = __float_as_uint(__uint_as_float(o[h][j][2 * x + (i & 1)]) * alpha);
-                } else if constexpr (HPW == 4) {
+                if constexpr (HPW == 4) {
                   o[h][j][2 * x] = __float_as_uint(__uint_as_float(o[h][j][2 * x]) * alpha);
-                  if (h == 0) o[h][j][2 * x + 1] = __float_as_uint(__uint_as_float(o[h][j][2 * x + 1]) * alpha);
-                } else {
+                  o[h][j][2 * x + 1] = __float_as_uint(__uint_as_float(o[h][j][2 * x + 1]) * alpha);
+                } else if (HPW == 8 || h == i >> 1) {
                   o[h][j][2 * x + (i & 1)] = __float_as_uint(__uint_as_float(o[h][j][2 * x + (i & 1)]) * alpha);
                 }
               }
@@ -701,7 +682,9 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
       for (int mt = 0; mt < 2; ++mt) {
         uint32_t p[2][C::kHL];  // parts of rows n and n + 8
 #pragma unroll
-        for (int i = 0; i < C::kHL; ++i) weight_parts<TYPE>(w[2 * mt][i], w[2 * mt + 1][i], &p[0][i], &p[1][i]);
+        for (int i = 0; i < C::kHL; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) p[r][i] = __float2uint_rn(w[2 * mt + r][i] * 8388608.f);  // w < 1.9 in 24 bits, three bytes
         if constexpr (HPW == 4) {
           // 16-bit columns 2t: part 0 | part 2 << 8, 2t + 1: part 1
           const uint32_t x = transpose_8x8(__byte_perm(p[0][0], 0u, 0x4102)), y = transpose_8x8(__byte_perm(p[1][0], 0u, 0x4102));
@@ -723,15 +706,33 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
         uint32_t v[4];  // dims 16 j + n, + 8 of tokens 4t .. 4t + 3, then of 16 more
         ldmatrix_bytes_trans_x2(v, v_read + off + ((j ^ v_sw) << 4));
 #pragma unroll
-        for (int h = 0; h < C::kOTiles; ++h) mma_8bit_16832<TYPE, true>(o[h][j], v, pf[h][0], pf[h][1]);
+        for (int h = 0; h < C::kOTiles; ++h) mma_8bit_16832<true>(o[h][j], v, pf[h][0], pf[h][1]);
       }
     } else {
-      uint32_t pf[C::kGroups][2][2];
+      uint32_t pf[C::kOTiles][2][2];
+      if constexpr (HPW == 4) {  // columns 2t: weight, 2t + 1: its rest
 #pragma unroll
-      for (int h = 0; h < C::kGroups; ++h)
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t hi, lo;
+          weight_halves(w[2 * mt][0], w[2 * mt + 1][0], &hi, &lo);
+          pf[0][mt][0] = transpose_8x8(__byte_perm(hi, lo, 0x5410));
+          pf[0][mt][1] = transpose_8x8(__byte_perm(hi, lo, 0x7632));
+        }
+      } else if constexpr (HPW == 8) {  // a tile of weights, one of rests
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          pf[h][r >> 1][r & 1] = transpose_8x8(pack_half2(w[r][(2 * h) % C::kHL], w[r][(2 * h + 1) % C::kHL]));
+        for (int r = 0; r < 4; ++r) {
+          uint32_t hi, lo;
+          weight_halves(w[r][0], w[r][C::kHL - 1], &hi, &lo);
+          pf[0][r >> 1][r & 1] = transpose_8x8(hi);
+          pf[C::kOTiles - 1][r >> 1][r & 1] = transpose_8x8(lo);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < C::kOTiles; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            pf[h][r >> 1][r & 1] = transpose_8x8(pack_half2(w[r][(2 * h) % C::kHL], w[r][(2 * h + 1) % C::kHL]));
+      }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         uint32_t v[4];
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
           const uint32_t f[4] = {codes_to_half2<TYPE, 0>(v[2 * mt]), codes_to_half2<TYPE, 0>(v[2 * mt + 1]),
                                  codes_to_half2<TYPE, 1>(v[2 * mt]), codes_to_half2<TYPE, 1>(v[2 * mt + 1])};
 #pragma unroll
-          for (int h = 0; h < C::kGroups; ++h) mma_f16_16816(reinterpret_cast<float*>(o[h][j]), f, pf[h][mt][0], pf[h][mt][1]);
+          for (int h = 0; h < C::kOTiles; ++h) mma_f16_16816(reinterpret_cast<float*>(o[h][j]), f, pf[h][mt][0], pf[h][mt][1]);
         }
       }
     }
