@@ -6,15 +6,22 @@
 // `index_block` tokens per (request, KV head) (1: the tokens an indexer
 // selects).
 //
-// Mathematics. Both products run on the 8-bit matrix instructions with the
-// codes as they lie in the cache, and the other operand cut into parts of the
-// cache's own type, which fill the columns that a decode group's few heads
-// leave free. q: in int8, q * S rounded to a 23-bit integer (S a power of two,
-// so bf16 values down to 2^-14 of the head's largest are exact), three signed base-256
-// digits; in e4m3, the rounding of q * S and the rounding of 16 times what it
-// left, which hold a bf16 value's 8 bits down to 2^-14 of the largest. The
-// weights: 24-bit fixed point as three unsigned bytes, or three e4m3 roundings, each
-// of 16 times what the one before left (12 bits). V's scale joins the
+// Mathematics. int8: both products run on the 8-bit matrix instructions with
+// the codes as they lie in the cache, and the other operand cut into bytes,
+// which fill the columns that a decode group's few heads leave free: q * S
+// rounded to a 23-bit integer (S a power of two, so bf16 values down to 2^-14
+// of the head's largest are exact) as three signed base-256 digits, the
+// weights in 24-bit fixed point as three unsigned bytes. (Unpacking codes to
+// fp16 instead took 80 to 140 integer instructions per 16 tokens, a third of
+// the loop.) e4m3: the 8-bit instruction takes as long as two fp16 ones after
+// a conversion that it repeats for every part, so codes are converted once,
+// exactly, and multiplied in fp16: q * S, exact down to 2^-27 of the largest,
+// in one part, the weight's rounding (11 bits) and 2^11 times the rest (11
+// more) in two (16 x 32768 tokens: 8-bit instructions 175 us, fp16 163; codes
+// moved to fp16 by shifts and masks 211). Groups of more than 8 query heads
+// would need more accumulators than there are registers: for them both
+// products run on fp16 in either type, with weights rounded to fp16 (2^-11).
+// V's scale joins the
 // exponent: with base-2 logits z and u_j = z_j + log2 sv_j, the weights a_j =
 // 2^(u_j - M) < 2 multiply V's codes, and the sum of a_j / sv_j = 2^(z_j - M), in fp32
 // from the weights before they are cut up, divides them at the end. One
@@ -22,11 +29,6 @@
 // only a value more than 0.9 above it moves it, so the common tile takes no
 // shuffle for the maximum and no rescale. int8 sums are int32 and join fp32
 // sums when M moves, and every kKaFoldTiles tiles, before they can overflow.
-// (Unpacking codes to fp16 instead took 80 to 140 integer instructions per 16 tokens, a third of
-// the loop, and left the fp16 instructions half empty.) Groups of more than 8
-// query heads would need more accumulators than there are registers: for
-// them P.V runs on fp16 instructions, with codes unpacked once for 16 heads
-// and weights rounded to fp16 (2^-11).
 //
 // Layout. Everything is warp-private: a warp owns up to 16 query heads of one
 // KV head and streams its tokens through a ring of 32-token cp.async stages
@@ -45,9 +47,9 @@
 // partials in closed form from the list. Ragged batches need no host
 // schedule. Bound by HBM where there is enough to read: 2 D bytes per token
 // and KV head. 32 query heads over 8 KV heads of 128: 16 x 32768 tokens (1075 MB) in
-// 163.3 us, 6.58 TB/s, the rate of a plain copy (e4m3 175 us: its matrix
-// instruction takes twice the tensor pipe's time, and more ALU work); 16
-// requests of 1040 to 9232 tokens (127 MB) 29.9 us; 1000 tokens 7.8 us, launches and trips to memory.
+// 163.3 us, 6.58 TB/s, the rate of a plain copy, in either type (64 query
+// heads 168 us int8 and 166 e4m3, 128 heads 211 and 190); 16
+// requests of 1040 to 9232 tokens (127 MB, e4m3) 28.2 us; 1000 tokens 7.8 us, launches and trips to memory.
 #pragma once
 
 #include "kv_store.cuh"
@@ -84,8 +86,7 @@ struct KvAttnArgs {
 // logits of kHL heads for the tokens of rows n and n + 8.
 template <int D, int HPW, int TYPE>
 struct KvAttnCfg {
-  static constexpr bool kHalf = TYPE == SD_KV_E4M3;      // q . k on fp16 instructions
-  static constexpr bool kBytes = !kHalf && HPW <= 8;     // P.V on 8-bit instructions
+  static constexpr bool kHalf = TYPE == SD_KV_E4M3 || HPW == 16;  // both products on fp16 instructions
   static constexpr int kParts = kHalf ? 1 : 3;
   // HPW 4: column 2t + x of S tile j is part 2j + x of head t (fp16: x = 0);
   // else tile (hg, p) is part p of heads 8 hg .. 8 hg + 7
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
   float qs[C::kHL];  // scale of this lane's heads (base-2 logits)
   float m[C::kHL], l[C::kHL];
   uint32_t o[C::kOTiles][D / 16][4] = {};  // int32 or fp32 sums; D / 16 tiles of 16 dims
-  constexpr bool kFold = C::kBytes && TYPE == SD_KV_INT8;
+  constexpr bool kFold = !C::kHalf;  // int32 sums
   float of[kFold ? C::kHL : 1][D / 16][2];  // what the int32 sums have been folded into
   int since = 0;                            // tiles since then
   auto lane_head = [&](int i) { return HPW == 4 ? t : (i >> 1) * 8 + 2 * t + (i & 1); };
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
       return fmaf(__uint_as_float(o[0][j][2 * x + 1]), 1.f / 2048.f, __uint_as_float(o[0][j][2 * x]));
     } else if constexpr (C::kHalf && HPW == 8) {
       return fmaf(__uint_as_float(o[C::kOTiles - 1][j][2 * x + (i & 1)]), 1.f / 2048.f, __uint_as_float(o[0][j][2 * x + (i & 1)]));
-    } else if constexpr (!C::kBytes) {
+    } else if constexpr (C::kHalf) {
       return __uint_as_float(o[i >> 1][j][2 * x + (i & 1)]);
     } else {
       const uint32_t p0 = HPW == 4 ? o[0][j][2 * x] : o[0][j][2 * x + (i & 1)];
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
 #pragma unroll
         for (int x = 0; x < (C::kHalf ? 2 : 1); ++x) {
           if constexpr (C::kHalf) {  // codes 0, 1 and 2, 3 of each word are the instruction's column pairs
-            const uint32_t w0 = f[2 * x], w1 = f[2 * x + 1];
+            const uint32_t w0 = bias_codes<TYPE>(f[2 * x]), w1 = bias_codes<TYPE>(f[2 * x + 1]);
             const uint32_t c[4] = {codes_to_half2<TYPE, 0>(w0), codes_to_half2<TYPE, 0>(w1), codes_to_half2<TYPE, 1>(w0),
                                    codes_to_half2<TYPE, 1>(w1)};
 #pragma unroll
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
 
     // ---- P: transposed so that a lane has its column's weights of the tokens
     // 4t .. 4t + 3 (+ 16), whose codes it holds ----
-    if constexpr (C::kBytes) {
+    if constexpr (!C::kHalf) {
       uint32_t pf[C::kOTiles][2];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
