@@ -360,8 +360,9 @@ typedef struct sd_kv_cache {
  * Arithmetic is fp32, angles fp64; q_out and bf16 pools are rounded once. In
  * an 8-bit pool the scale of a (block, KV head) is
  *   max(amax(new rows) / qmax, the scale it had if it holds earlier tokens, 2^-100)
- * (qmax 127 or 448), codes are round(y / scale), and earlier codes of a block
- * whose scale grew are coded anew, round(code * old / new). NaN is stored as
+ * (qmax 127 or 448), codes are round(y / scale) of the fp32 quotient, ties to
+ * even, and earlier codes of a block whose scale grew are coded anew,
+ * round(code * (old / new)). NaN is stored as
  * code 0 and an infinity as the largest code; neither enters the scale.
  * k_bounds of a block are those of its tokens' bf16 keys. Pool rows, scales and bounds
  * of other blocks are not touched; two requests must not share a block that

@@ -14,7 +14,7 @@
 // and one for V:
 //   s = max(amax(new rows) / qmax, s of the block's earlier rows, 2^-100)
 // with qmax 127 or 448, codes round(y / s), and the earlier rows of a block
-// whose scale grew coded anew, round(code * s_old / s_new). A growing scale
+// whose scale grew coded anew, round(code * (s_old / s_new)). A growing scale
 // costs an earlier row one more rounding each time it grows, and never
 // clips a later token. Entries that are not finite do not enter the scale:
 // NaN is coded as 0, infinities as the largest code.
@@ -28,9 +28,9 @@
 // and units of several rows fall back to the whole CTA. q: one group of D / 8 lanes per (token,
 // group of heads); the token's angles are computed once per group and used
 // for its heads. 32 query heads over 8 KV heads of 128: four prompts into int8
-// (212 MB of q, 40 M instructions) 62 us, bound by issue slots (65 % used) and
-// then HBM; three prompts into bf16 32.7 us; one token 3.7 us and 64 tokens
-// 4.7 us, bound by launch and load latency.
+// (212 MB of q, 40 M instructions) 64 us, bound by issue slots (65 % used) and
+// then HBM; three prompts into bf16 32.8 us; one token 3.7 us and 64 tokens
+// 4.6 us, bound by launch and load latency.
 #pragma once
 
 #include <float.h>
@@ -204,14 +204,18 @@ struct Rotation {
   }
 };
 
-// Four codes round(e * inv), any input: NaN is 0, infinities the largest code.
-__device__ __noinline__ uint32_t encode4_any(float e0, float e1, float e2, float e3, float inv, int kv_type) {
+// Codes are round(y / s) of the fp32 quotient: bf16 values divided by a scale
+// that came from one of them meet exact ties, and y * (1 / s), one rounding
+// more, sends some of them to the wrong neighbour.
+//
+// Four codes round(e / s), any input: NaN is 0, infinities the largest code.
+__device__ __noinline__ uint32_t encode4_any(float e0, float e1, float e2, float e3, float s, int kv_type) {
   const float e[4] = {e0, e1, e2, e3};
   if (kv_type == SD_KV_INT8) {
     uint32_t w = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int c = max(-127, min(127, __float2int_rn(e[j] * inv)));  // NaN converts to 0
+      const int c = max(-127, min(127, __float2int_rn(e[j] / s)));  // NaN converts to 0
       w |= (static_cast<uint32_t>(c) & 0xffu) << (8 * j);
     }
     return w;
@@ -219,7 +223,7 @@ __device__ __noinline__ uint32_t encode4_any(float e0, float e1, float e2, float
   float z[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    z[j] = e[j] * inv;
+    z[j] = e[j] / s;
     z[j] = z[j] == z[j] ? z[j] : 0.f;
   }
   const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(z[0], z[1]), __NV_SATFINITE, __NV_E4M3);
@@ -227,22 +231,38 @@ __device__ __noinline__ uint32_t encode4_any(float e0, float e1, float e2, float
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-__device__ __forceinline__ uint32_t encode4(const float* e, float inv, int kv_type) {
-  return encode4_any(e[0], e[1], e[2], e[3], inv, kv_type);
-}
-
-// The same for finite e with |e * inv| <= 127 in int8: adding 1.5 * 2^23
-// rounds to a whole number (to even) whose low byte is the code.
-__device__ __forceinline__ uint32_t encode4_finite(const float* e, float inv, int kv_type) {
+// Four codes of z, finite and in int8 at most 127 in magnitude: adding 1.5 *
+// 2^23 rounds to a whole number (to even) whose low byte is the code.
+__device__ __forceinline__ uint32_t round4(const float* z, int kv_type) {
   if (kv_type == SD_KV_INT8) {
     uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(fmaf(e[j], inv, 12582912.f));
+    for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(__fadd_rn(z[j], 12582912.f));
     return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
   }
-  const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(e[0] * inv, e[1] * inv), __NV_SATFINITE, __NV_E4M3);
-  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(e[2] * inv, e[3] * inv), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(z[0], z[1]), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(z[2], z[3]), __NV_SATFINITE, __NV_E4M3);
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// Whether encode4_finite holds for this scale: its products stay normal.
+__device__ __forceinline__ bool plain_scale(float s) { return s >= 8.67361738e-19f && s <= 1.2676506e30f; }  // 2^-60, 2^100
+
+// The codes of encode4_any for finite e and a plain scale, inv = 1 / s. The
+// quotient by one residual step (P. Markstein, IBM J. Res. Dev. 34, 1990): q =
+// e * inv is off by two units at most, e - q s is exact but for its last bit,
+// and what it adds leaves an error of 2^-22 units before the last rounding, so
+// that a quotient that is an fp32 number, an exact tie among them, comes out as that
+// number. (One that is below 2^-11 loses its residual's low bits, and rounds to
+// code 0 all the same.)
+__device__ __forceinline__ uint32_t encode4_finite(const float* e, float s, float inv, int kv_type) {
+  float z[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float q = __fmul_rn(e[j], inv);
+    z[j] = __fmaf_rn(__fmaf_rn(-q, s, e[j]), inv, q);
+  }
+  return round4(z, kv_type);
 }
 
 __device__ __forceinline__ void decode4(uint32_t w, int kv_type, float* e) {
@@ -276,22 +296,24 @@ __device__ __noinline__ void recode_rows(uint8_t* first, long long pitch, int n,
     for (int j = 0; j < 4; ++j) {
       float e[4];
       decode4(u[j], kv_type, e);
-      u[j] = encode4_finite(e, ratio, kv_type);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = __fmul_rn(e[i], ratio);
+      u[j] = round4(e, kv_type);
     }
     *at = w;
   }
 }
 
 template <int D, bool FINITE = false>
-__device__ __forceinline__ void store_row(void* pages, long long row, int l, const float* e, float inv, int kv_type) {
+__device__ __forceinline__ void store_row(void* pages, long long row, int l, const float* e, float s, float inv, int kv_type) {
   if (kv_type == SD_KV_BF16) {
     __nv_bfloat16* at = static_cast<__nv_bfloat16*>(pages) + row * D;
     *reinterpret_cast<uint2*>(at + 4 * l) = make_uint2(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]));
     *reinterpret_cast<uint2*>(at + D / 2 + 4 * l) = make_uint2(pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7]));
   } else {
     uint8_t* at = static_cast<uint8_t*>(pages) + row * D;
-    *reinterpret_cast<uint32_t*>(at + 4 * l) = FINITE ? encode4_finite(e, inv, kv_type) : encode4(e, inv, kv_type);
-    *reinterpret_cast<uint32_t*>(at + D / 2 + 4 * l) = FINITE ? encode4_finite(e + 4, inv, kv_type) : encode4(e + 4, inv, kv_type);
+    *reinterpret_cast<uint32_t*>(at + 4 * l) = FINITE ? encode4_finite(e, s, inv, kv_type) : encode4_any(e[0], e[1], e[2], e[3], s, kv_type);
+    *reinterpret_cast<uint32_t*>(at + D / 2 + 4 * l) = FINITE ? encode4_finite(e + 4, s, inv, kv_type) : encode4_any(e[4], e[5], e[6], e[7], s, kv_type);
   }
 }
 
@@ -350,7 +372,7 @@ __device__ void store_queries(const KvStoreArgs& a, int cta) {
       unpack_row<D>(x[j], y[j], e);
       if (a.qw != nullptr) norm_row<D>(e, w, a.eps);
       if (a.R > 0) rot.apply(e, a.R, a.interleaved, l);
-      if (ok && h < h1 && i + j < a.heads_per_group) store_row<D>(dst, h, l, e, 1.f, SD_KV_BF16);
+      if (ok && h < h1 && i + j < a.heads_per_group) store_row<D>(dst, h, l, e, 1.f, 1.f, SD_KV_BF16);
     }
   }
 }
@@ -480,7 +502,7 @@ __device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBl
         *reinterpret_cast<float4*>(at + D / 2) = make_float4(e[4], e[5], e[6], e[7]);
       } else {
         const long long row = (u.base + (u.lo - u.c * bs) + i) * geo.G + g;
-        store_row<D>(a.k_pages, row, l, e, 1.f, SD_KV_BF16);
+        store_row<D>(a.k_pages, row, l, e, 1.f, 1.f, SD_KV_BF16);
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.v_pages) + row * D + 4 * l;
         *reinterpret_cast<uint2*>(dst) = vx;
         *reinterpret_cast<uint2*>(dst + D / 2) = vy;
@@ -542,6 +564,7 @@ __device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBl
     }
     if (tid == 0) a.k_scales[u.blk] = sk, a.v_scales[u.blk] = sv;
     const float ik = 1.f / sk, iv = 1.f / sv;
+    const bool plain = finite && plain_scale(sk) && plain_scale(sv);
     const long long first = (u.base + (u.lo - u.c * bs)) * geo.G + g;
 #pragma unroll 1
     for (int i = tid / LANES; i < u.nr; i += RPP) {
@@ -553,12 +576,12 @@ __device__ void store_unit_cta(const KvStoreArgs& a, const KvUnit u, int g, KvBl
       const long long row = first + (long long)i * geo.G;
       float v[8];
       unpack_row<D>(vx, vy, v);
-      if (finite) {
-        store_row<D, true>(a.k_pages, row, l, e, ik, a.kv_type);
-        store_row<D, true>(a.v_pages, row, l, v, iv, a.kv_type);
+      if (plain) {
+        store_row<D, true>(a.k_pages, row, l, e, sk, ik, a.kv_type);
+        store_row<D, true>(a.v_pages, row, l, v, sv, iv, a.kv_type);
       } else {
-        store_row<D>(a.k_pages, row, l, e, ik, a.kv_type);
-        store_row<D>(a.v_pages, row, l, v, iv, a.kv_type);
+        store_row<D>(a.k_pages, row, l, e, sk, ik, a.kv_type);
+        store_row<D>(a.v_pages, row, l, v, sv, iv, a.kv_type);
       }
     }
   }
@@ -611,18 +634,19 @@ __device__ void store_unit_warp(const KvStoreArgs& a, const KvUnit& u, int g, ui
     rot.apply(e, a.R, a.interleaved, l);
   }
   float m = 0.f;
+  bool finite = true;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     e[j] = is_v ? v[j] : e[j];
     m = fmaxf(m, finite_abs(e[j]));
+    finite &= fabsf(e[j]) <= FLT_MAX;
   }
-  float inv = 1.f;
+  float s = 1.f;
   if (quant) {
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float qmax = a.kv_type == SD_KV_INT8 ? 127.f : 448.f;
-    const float s = fmaxf(fmaxf(m / qmax, kKvMinScale), old);
-    inv = 1.f / s;
+    s = fmaxf(fmaxf(m / qmax, kKvMinScale), old);
     if (earlier) {
       const float sk = __shfl_sync(0xffffffffu, s, 0), sv = __shfl_sync(0xffffffffu, s, LANES);
       const float ok = __shfl_sync(0xffffffffu, old, 0), ov = __shfl_sync(0xffffffffu, old, LANES);
@@ -633,7 +657,11 @@ __device__ void store_unit_warp(const KvStoreArgs& a, const KvUnit& u, int g, ui
     }
     if (live && l == 0) scales[u.blk] = s;
   }
-  if (live) store_row<D>(pages, (u.base + (u.lo - u.c * bs)) * geo.G + g, l, e, inv, a.kv_type);
+  const long long row = (u.base + (u.lo - u.c * bs)) * geo.G + g;
+  if (live) {
+    if (finite && plain_scale(s)) store_row<D, true>(pages, row, l, e, s, 1.f / s, a.kv_type);
+    else store_row<D>(pages, row, l, e, s, 1.f, a.kv_type);
+  }
   if (a.bounds == nullptr || lane >= LANES) return;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
