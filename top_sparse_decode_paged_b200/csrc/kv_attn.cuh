@@ -11,24 +11,35 @@
 // which fill the columns that a decode group's few heads leave free: q * S
 // rounded to a 23-bit integer (S a power of two, so bf16 values down to 2^-14
 // of the head's largest are exact) as three signed base-256 digits, the
-// weights in 24-bit fixed point as three unsigned bytes. (Unpacking codes to
-// fp16 instead took 80 to 140 integer instructions per 16 tokens, a third of
-// the loop.) e4m3: the 8-bit instruction takes as long as two fp16 ones after
-// a conversion that it repeats for every part, so codes are converted once,
-// exactly, and multiplied in fp16: q * S, exact down to 2^-27 of the largest,
-// in one part, the weight's rounding (11 bits) and 2^11 times the rest (11
-// more) in two (16 x 32768 tokens: 8-bit instructions 175 us, fp16 163; codes
-// moved to fp16 by shifts and masks 211). Groups of more than 8 query heads
-// would need more accumulators than there are registers: for them both
-// products run on fp16 in either type, with weights rounded to fp16 (2^-11).
-// V's scale joins the
-// exponent: with base-2 logits z and u_j = z_j + log2 sv_j, the weights a_j =
-// 2^(u_j - M) < 2 multiply V's codes, and the sum of a_j / sv_j = 2^(z_j - M), in fp32
-// from the weights before they are cut up, divides them at the end. One
-// reference M serves both, and it follows the running maximum of u lazily:
-// only a value more than 0.9 above it moves it, so the common tile takes no
-// shuffle for the maximum and no rescale. int8 sums are int32 and join fp32
-// sums when M moves, and every kKaFoldTiles tiles, before they can overflow.
+// weights in fixed point as unsigned bytes: four (32 bits) for up to 4 heads,
+// where the fourth lies in a column that is free anyway; three (24 bits) for
+// up to 8, with the fourth rounded into them by a sequence that goes evenly
+// over its range. (Rounded to the nearest, weights below 2^-24 were lost
+// altogether, and 2^18 of them beside a large one are a hundredth of the sum.
+// Four bytes for 8 heads: 64 query heads 192 us instead of 171.) (Unpacking
+// codes to fp16 instead took 80 to 140 integer instructions per 16 tokens, a
+// third of the loop.) e4m3: the 8-bit instruction takes as long as two fp16
+// ones after a conversion that it repeats for every part, so codes are
+// converted once, exactly, and multiplied in fp16: q * S, exact down to 2^-27
+// of the largest, in one part, the weight's rounding (11 bits) and 2^11 times
+// the rest (11 more) in two, both times 2^14 so that small weights stay
+// normal (16 x 32768 tokens: 8-bit instructions 175 us, fp16 163; codes moved
+// to fp16 by shifts and masks 211). Groups of more than 8 query heads would
+// need more accumulators than there are registers: for them both products run
+// on fp16 in either type, with weights of 11 bits, times 2^14: off by 2^-11
+// of the weighted |v| at most, a quarter of the output's own rounding where
+// the values do not cancel.
+// V's scale joins the exponent: with base-2 logits z and u_j = z_j + log2
+// sv_j, the weights a_j = 2^(u_j - M) < 2 multiply V's codes, and the sum of
+// a_j / sv_j = 2^(z_j - M), in fp32 from the weights before they are cut up,
+// divides them at the end. One reference M serves both, and it follows the
+// running maximum of u lazily: only a value more than 0.9 above it moves it,
+// so the common tile takes no shuffle for the maximum and no rescale. int8
+// sums are int32 and join fp32 sums when M moves, and every kKaFoldTiles
+// tiles, before they can overflow; the sums of weights are taken over
+// kKaSumTiles tiles and then added up. The fp16 instructions cut their fp32
+// sums at 2^-23 with every 16 tokens: n tokens in a range lose n * 2^-27 of
+// their sum at most, an output's rounding at 2^18 of them.
 //
 // Layout. Everything is warp-private: a warp owns up to 16 query heads of one
 // KV head and streams its tokens through a ring of 32-token cp.async stages
@@ -48,7 +59,7 @@
 // schedule. Bound by HBM where there is enough to read: 2 D bytes per token
 // and KV head. 32 query heads over 8 KV heads of 128: 16 x 32768 tokens (1075 MB) in
 // 163.3 us, 6.58 TB/s, the rate of a plain copy, in either type (64 query
-// heads 168 us int8 and 166 e4m3, 128 heads 211 and 190); 16
+// heads 171 us int8 and 166 e4m3, 128 heads 226 and 191); 16
 // requests of 1040 to 9232 tokens (127 MB, e4m3) 28.2 us; 1000 tokens 7.8 us, launches and trips to memory.
 #pragma once
 
@@ -63,6 +74,7 @@ constexpr int kKaTile = 32;        // tokens per warp and stage: one row lookup 
 constexpr int kKaRanges = 148;     // CTAs of a column group in one wave: one per SM
 constexpr float kKaSlack = 0.9f;   // log2: how far a weight may pass the running reference
 constexpr int kKaFoldTiles = 1024; // int32 sums: 1024 x 32 x 255 x 128 < 2^31
+constexpr int kKaSumTiles = 64;    // fp32 sums of weights: small ones beside a large one are lost for so long at most
 
 struct KvAttnArgs {
   const __nv_bfloat16* q;
@@ -94,8 +106,9 @@ struct KvAttnCfg {
   static constexpr int kQSteps = D / (kHalf ? 16 : 32);  // instructions along D
   // O likewise, with the three parts of the weights; fp16: HPW 4: the weight
   // and its rest, HPW 8: a tile of each, HPW 16: head groups
-  static constexpr int kOTiles = kHalf ? (HPW == 4 ? 1 : 2) : HPW == 4 ? 2 : HPW == 8 ? 3 : 2;
+  static constexpr int kOTiles = kHalf ? (HPW == 4 ? 1 : 2) : HPW == 4 ? 2 : 3;
   static constexpr int kHL = HPW == 4 ? 1 : HPW / 4;
+  static constexpr float kUp = kHalf ? 14.f : 0.f;  // fp16 weights are held times 2^14: below 2^15, normal down to 2^-28
   static constexpr int kGroups = HPW == 16 ? 2 : 1;
   static constexpr int kRowBytes = kKaTile * D;                   // K (or V) of a stage
   static constexpr int kStage = 2 * kRowBytes + 2 * kKaTile * 4;  // + the tokens' scales
@@ -403,27 +416,32 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
   int cb = b_begin, ctile = tile_begin, clen = kv_attn_len(a, cb);
   uint32_t qf[C::kSTiles][C::kQSteps][2];
   float qs[C::kHL];  // scale of this lane's heads (base-2 logits)
-  float m[C::kHL], l[C::kHL];
+  float m[C::kHL];                // log2 of what a weight of 1 stands for: M - kUp
+  float l[C::kHL], ls[C::kHL];    // sums of weights: the last tiles', and those before
   uint32_t o[C::kOTiles][D / 16][4] = {};  // int32 or fp32 sums; D / 16 tiles of 16 dims
   constexpr bool kFold = !C::kHalf;  // int32 sums
   float of[kFold ? C::kHL : 1][D / 16][2];  // what the int32 sums have been folded into
-  int since = 0;                            // tiles since then
+  int since = 0;                            // tiles since then, or since M moved
   auto lane_head = [&](int i) { return HPW == 4 ? t : (i >> 1) * 8 + 2 * t + (i & 1); };
+  constexpr float kDown = 1.f / 16384.f;  // 2^-kUp
+  constexpr uint32_t kGolden = 0x9e3779b9u;  // 2^32 over the golden ratio
   // sum of this lane's head i, dim 16 j + n + 8 x, in units of its weights and codes
   auto sum_of = [&](int i, int j, int x) {
     if constexpr (C::kHalf && HPW == 4) {  // the rests are in units of 2^-11
-      return fmaf(__uint_as_float(o[0][j][2 * x + 1]), 1.f / 2048.f, __uint_as_float(o[0][j][2 * x]));
+      return fmaf(__uint_as_float(o[0][j][2 * x + 1]), kDown / 2048.f, __uint_as_float(o[0][j][2 * x]) * kDown);
     } else if constexpr (C::kHalf && HPW == 8) {
-      return fmaf(__uint_as_float(o[C::kOTiles - 1][j][2 * x + (i & 1)]), 1.f / 2048.f, __uint_as_float(o[0][j][2 * x + (i & 1)]));
+      return fmaf(__uint_as_float(o[C::kOTiles - 1][j][2 * x + (i & 1)]), kDown / 2048.f, __uint_as_float(o[0][j][2 * x + (i & 1)]) * kDown);
     } else if constexpr (C::kHalf) {
-      return __uint_as_float(o[i >> 1][j][2 * x + (i & 1)]);
+      return __uint_as_float(o[i >> 1][j][2 * x + (i & 1)]) * kDown;
     } else {
-      const uint32_t p0 = HPW == 4 ? o[0][j][2 * x] : o[0][j][2 * x + (i & 1)];
-      const uint32_t p1 = HPW == 4 ? o[0][j][2 * x + 1] : o[1][j][2 * x + (i & 1)];
-      const uint32_t p2 = HPW == 4 ? o[1][j][2 * x] : o[C::kOTiles - 1][j][2 * x + (i & 1)];
-      // digits of 2^-23
-      return fmaf(static_cast<float>(static_cast<int>(p0)), 0.0078125f,
-                  fmaf(static_cast<float>(static_cast<int>(p1)), 0.0078125f / 256.f, static_cast<float>(static_cast<int>(p2)) * (0.0078125f / 65536.f)));
+      const int k = HPW == 4 ? 2 * x : 2 * x + (i & 1);
+      const float p0 = static_cast<float>(static_cast<int>(o[0][j][k]));
+      const float p1 = static_cast<float>(static_cast<int>(HPW == 4 ? o[0][j][k + 1] : o[1][j][k]));
+      const float p2 = static_cast<float>(static_cast<int>(HPW == 4 ? o[1][j][k] : o[C::kOTiles - 1][j][k]));
+      float low = p2;
+      if constexpr (HPW == 4) low = fmaf(static_cast<float>(static_cast<int>(o[1][j][k + 1])), 1.f / 256.f, p2);
+      // digits of 2^-7, 2^-15, 2^-23 and 2^-31
+      return fmaf(p0, 0.0078125f, fmaf(p1, 0.0078125f / 256.f, low * (0.0078125f / 65536.f)));
     }
   };
   uint32_t qraw[C::kGroups][D / 8];  // dims 16 kk + 4t .. + 3 in words 2 kk, 2 kk + 1 of head n (HPW 4: n / 2)
@@ -482,14 +500,14 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
     for (int i = 0; i < C::kHL; ++i) {
       qs[i] = __shfl_sync(0xffffffffu, back_of[HPW == 4 ? 0 : i >> 1], (HPW == 4 ? 2 * t : 2 * t + (i & 1)) * 4);
       m[i] = -INFINITY;
-      l[i] = 0.f;
+      l[i] = ls[i] = 0.f;
     }
+    since = 0;
 #pragma unroll
     for (int h = 0; h < C::kOTiles; ++h)
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) o[h][j][0] = o[h][j][1] = o[h][j][2] = o[h][j][3] = 0u;
     if constexpr (kFold) {
-      since = 0;
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i)
 #pragma unroll
@@ -500,14 +518,14 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
     const size_t slot = ((size_t)range + b) * a.spw + sub;
 #pragma unroll
     for (int i = 0; i < C::kHL; ++i) {
-      float s = l[i];
+      float s = l[i] + ls[i];
       s += __shfl_xor_sync(0xffffffffu, s, 4);
       s += __shfl_xor_sync(0xffffffffu, s, 8);
       s += __shfl_xor_sync(0xffffffffu, s, 16);
       const int h = lane_head(i);
       if (h >= nh) continue;
       const size_t at = slot * a.H + h0 + h;
-      if (n == 0) a.part_ml[at] = make_float2(m[i], s);
+      if (n == 0) a.part_ml[at] = make_float2(m[i] + C::kUp, s);
       float* dst = a.part_o + at * D + n;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
@@ -604,13 +622,17 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
 
     // ---- weights: w[r] is token tk + 2 (r & 1) + 16 (r >> 1) ----
     float w[4][C::kHL], isv[4];
-    bool over = kFold && ++since >= kKaFoldTiles;
+    bool over = kFold && since >= kKaFoldTiles;
+    if ((++since & (kKaSumTiles - 1)) == 0) {
+#pragma unroll
+      for (int i = 0; i < C::kHL; ++i) ls[i] += l[i], l[i] = 0.f;
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int k = tk + 2 * (r & 1) + 16 * (r >> 1), x = 2 * (r & 1);
       const float ks = sc[k], vs = fmaxf(sc[kKaTile + k], kKvMinScale);
       const float lv = fast_log2(vs);
-      isv[r] = __fdividef(1.f, vs);
+      isv[r] = __fdividef(C::kHalf ? kDown : 1.f, vs);
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i) {
         const uint32_t(*p)[4] = s[r >> 1] + (HPW == 4 ? 0 : (i >> 1) * C::kParts);
@@ -623,21 +645,22 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
           z = fmaf(static_cast<float>(static_cast<int>(p0) * 256 + static_cast<int>(p1)), 256.f, static_cast<float>(static_cast<int>(p2)));
         }
         w[r][i] = ks >= 0.f ? fmaf(z, qs[i] * ks, lv) : -INFINITY;  // u
-        over |= w[r][i] > m[i] + kKaSlack;
+        over |= w[r][i] > m[i] + (kKaSlack + C::kUp);
       }
     }
     if (__any_sync(0xffffffffu, over)) {
-      since = 0;
+      since = 1;
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i) {
         float mx = fmaxf(fmaxf(w[0][i], w[1][i]), fmaxf(w[2][i], w[3][i]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        mx = fmaxf(mx, m[i]);
+        mx = fmaxf(mx - C::kUp, m[i]);
         const float alpha = mx == -INFINITY ? 1.f : fast_exp2(m[i] - mx);
         m[i] = mx;
-        l[i] *= alpha;
+        ls[i] = (ls[i] + l[i]) * alpha;
+        l[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
 #pragma unroll
@@ -679,23 +702,29 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
     // 4t .. 4t + 3 (+ 16), whose codes it holds ----
     if constexpr (!C::kHalf) {
       uint32_t pf[C::kOTiles][2];
+      const uint32_t weyl = kGolden * (at * kKaTile + tk);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         uint32_t p[2][C::kHL];  // parts of rows n and n + 8
 #pragma unroll
-        for (int i = 0; i < C::kHL; ++i)
+        for (int r = 0; r < 2; ++r) {
+          // three parts of four: the last byte is rounded up as often as its
+          // value says, by the multiples of the golden ratio (H. Weyl's
+          // sequence), so that weights below 2^-24 are lost singly, not in sum
+          const uint32_t up = HPW == 4 ? 0u : (weyl + kGolden * (2 * r + 16 * mt)) >> 24;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) p[r][i] = __float2uint_rn(w[2 * mt + r][i] * 8388608.f);  // w < 1.9 in 24 bits, three bytes
+          for (int i = 0; i < C::kHL; ++i) p[r][i] = __float2uint_rn(w[2 * mt + r][i] * 2147483648.f) + up;  // w < 1.9
+        }
         if constexpr (HPW == 4) {
-          // 16-bit columns 2t: part 0 | part 2 << 8, 2t + 1: part 1
-          const uint32_t x = transpose_8x8(__byte_perm(p[0][0], 0u, 0x4102)), y = transpose_8x8(__byte_perm(p[1][0], 0u, 0x4102));
+          // 16-bit columns 2t: part 0 | part 2 << 8, 2t + 1: part 1 | part 3 << 8
+          const uint32_t x = transpose_8x8(__byte_perm(p[0][0], 0u, 0x0213)), y = transpose_8x8(__byte_perm(p[1][0], 0u, 0x0213));
           pf[0][mt] = __byte_perm(x, y, 0x6420);
           pf[1][mt] = __byte_perm(x, y, 0x7531);
         } else {
           // columns 2t + i: part 0 | part 1 << 8 of head i; then part 2 of both rows
-          const uint32_t x = transpose_8x8(__byte_perm(p[0][0], p[0][C::kHL - 1], 0x5612));
-          const uint32_t y = transpose_8x8(__byte_perm(p[1][0], p[1][C::kHL - 1], 0x5612));
-          const uint32_t z = transpose_8x8(__byte_perm(__byte_perm(p[0][0], p[1][0], 0x0040), __byte_perm(p[0][C::kHL - 1], p[1][C::kHL - 1], 0x0040), 0x5410));
+          const uint32_t x = transpose_8x8(__byte_perm(p[0][0], p[0][C::kHL - 1], 0x6723));
+          const uint32_t y = transpose_8x8(__byte_perm(p[1][0], p[1][C::kHL - 1], 0x6723));
+          const uint32_t z = transpose_8x8(__byte_perm(__byte_perm(p[0][0], p[1][0], 0x0051), __byte_perm(p[0][C::kHL - 1], p[1][C::kHL - 1], 0x0051), 0x5410));
           pf[0][mt] = __byte_perm(x, y, 0x6420);
           pf[1][mt] = __byte_perm(x, y, 0x7531);
           pf[C::kOTiles - 1][mt] = __byte_perm(z, 0u, 0x3120);
