@@ -91,3 +91,34 @@ def test_products_that_cancel(kind, qpk):
         half = w.astype(np.float16).astype(np.float64)
         assert (np.abs(half @ v / w.sum() - ref) > 4 * tol).any()
     assert (np.abs(out - ref) <= tol).all(), (np.abs(out - ref) / mass).max()
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("qpk", [1, 5, 16])
+@pytest.mark.parametrize("G", [1, 1184])
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("sv,zero", [(2.0 ** 20, 0.0), (2.0 ** 60, 2.0 ** -100), (2.0 ** 110, 2.0 ** -43)])
+def test_zero_values_beside_large_ones(kind, qpk, G, first, sv, zero):
+    """One token with a large V scale and half of the softmax; the other half
+    belongs to 4095 tokens whose V is zero. Together with V scales the weights
+    are 2^130 and more apart. One KV head: partials of many warps; 1184: one
+    warp walks all tokens. The output's rounding 2^-8, weights and sums 2^-14."""
+    import torch
+    import top_sparse_decode_paged_b200 as sd
+    D, P, L = 64, 64, 4096
+    c = CODE[kind]
+    k, v = np.zeros((3, P, G, D), np.float32), np.zeros((3, P, G, D), np.float32)
+    at = 0 if first else P - 1
+    page = 0 if first else 2
+    k[page, at, :, 0], v[page, at] = c, c
+    scales = torch.full((3, 1, G), zero, device="cuda")
+    scales[page] = sv
+    cache = sd.KvCache(_pool(k, kind), _pool(v, kind), torch.ones((3, 1, G), device="cuda"), scales)
+    table = torch.ones((1, L // P), dtype=torch.int32)
+    table[0, 0], table[0, -1] = 0, 2
+    scale = np.log(L - 1) / c
+    lse = torch.empty((1, G * qpk), device="cuda")
+    out = sd.sd_kv_attn(_first_dim_queries(1, G * qpk, D), cache, table.cuda(), torch.tensor([L], dtype=torch.int32).cuda(), scale, lse=lse)
+    got, want = f64(out), 0.5 * c * sv
+    assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -14) * want).all(), (got.min() / want, got.max() / want)
+    assert (np.abs(f64(lse) - np.log(2 * (L - 1))) <= 2.0 ** -14).all(), f64(lse).ravel()[:4]

@@ -31,8 +31,7 @@
 // the values do not cancel.
 // V's scale joins the exponent: with base-2 logits z and u_j = z_j + log2
 // sv_j, the weights a_j = 2^(u_j - M) < 2 multiply V's codes, and the sum of
-// a_j / sv_j = 2^(z_j - M), in fp32 from the weights before they are cut up,
-// divides them at the end. One reference M serves both, and it follows the
+// 2^(z_j - M), in fp32, divides them at the end. One reference M serves both, and it follows the
 // running maximum of u lazily: only a value more than 0.9 above it moves it,
 // so the common tile takes no shuffle for the maximum and no rescale. int8
 // sums are int32 and join fp32 sums when M moves, and every kKaFoldTiles
@@ -59,7 +58,7 @@
 // schedule. Bound by HBM where there is enough to read: 2 D bytes per token
 // and KV head. 32 query heads over 8 KV heads of 128: 16 x 32768 tokens (1075 MB) in
 // 163.3 us, 6.58 TB/s, the rate of a plain copy, in either type (64 query
-// heads 171 us int8 and 166 e4m3, 128 heads 226 and 191); 16
+// heads 171 us int8 and 166 e4m3, 128 heads 226 and 186); 16
 // requests of 1040 to 9232 tokens (127 MB, e4m3) 28.2 us; 1000 tokens 7.8 us, launches and trips to memory.
 #pragma once
 
@@ -416,12 +415,18 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
   int cb = b_begin, ctile = tile_begin, clen = kv_attn_len(a, cb);
   uint32_t qf[C::kSTiles][C::kQSteps][2];
   float qs[C::kHL];  // scale of this lane's heads (base-2 logits)
+  // Whether the sum of weights takes 2^(z - M) itself, and not w / sv. w may
+  // be below fp32's range where w / sv is not; but while every V scale met lies
+  // between 2^-43 and 2^15, what that loses is below 2^-97 and the sum above
+  // 2^-15. (Groups of up to 8 heads always take it themselves, at no cost; with
+  // 16 heads each, 128 query heads 186 us so and 200 always, in e4m3.)
+  bool wide = HPW != 16;
   float m[C::kHL];                // log2 of what a weight of 1 stands for: M - kUp
   float l[C::kHL], ls[C::kHL];    // sums of weights: the last tiles', and those before
   uint32_t o[C::kOTiles][D / 16][4] = {};  // int32 or fp32 sums; D / 16 tiles of 16 dims
   constexpr bool kFold = !C::kHalf;  // int32 sums
   float of[kFold ? C::kHL : 1][D / 16][2];  // what the int32 sums have been folded into
-  int since = 0;                            // tiles since then, or since M moved
+  int since = 0;                            // tiles since then
   auto lane_head = [&](int i) { return HPW == 4 ? t : (i >> 1) * 8 + 2 * t + (i & 1); };
   constexpr float kDown = 1.f / 16384.f;  // 2^-kUp
   constexpr uint32_t kGolden = 0x9e3779b9u;  // 2^32 over the golden ratio
@@ -502,12 +507,13 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
       m[i] = -INFINITY;
       l[i] = ls[i] = 0.f;
     }
-    since = 0;
+    wide = HPW != 16;
 #pragma unroll
     for (int h = 0; h < C::kOTiles; ++h)
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) o[h][j][0] = o[h][j][1] = o[h][j][2] = o[h][j][3] = 0u;
     if constexpr (kFold) {
+      since = 0;
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i)
 #pragma unroll
@@ -525,7 +531,12 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
       const int h = lane_head(i);
       if (h >= nh) continue;
       const size_t at = slot * a.H + h0 + h;
-      if (n == 0) a.part_ml[at] = make_float2(m[i] + C::kUp, s);
+      // V scales far from one leave s far from one: its power of two moves
+      // into M, by which the combine weighs partials
+      int e = s > 0.f && s < INFINITY ? min(static_cast<int>(__float_as_uint(s) >> 23), 253) - 127 : 0;
+      if (abs(e) <= 32) e = 0;
+      const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      if (n == 0) a.part_ml[at] = make_float2(m[i] + static_cast<float>(e), s * f);
       float* dst = a.part_o + at * D + n;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
@@ -533,7 +544,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
         for (int x = 0; x < 2; ++x) {
           float v = sum_of(i, j, x);
           if constexpr (kFold) v += of[i][j][x];
-          dst[16 * j + 8 * x] = v;
+          dst[16 * j + 8 * x] = v * f;
         }
       }
     }
@@ -621,9 +632,9 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
     }
 
     // ---- weights: w[r] is token tk + 2 (r & 1) + 16 (r >> 1) ----
-    float w[4][C::kHL], isv[4];
-    bool over = kFold && since >= kKaFoldTiles;
-    if ((++since & (kKaSumTiles - 1)) == 0) {
+    float w[4][C::kHL], lv[4];
+    bool over = kFold && ++since >= kKaFoldTiles;
+    if ((at & (kKaSumTiles - 1)) == kKaSumTiles - 1) {
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i) ls[i] += l[i], l[i] = 0.f;
     }
@@ -631,8 +642,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
     for (int r = 0; r < 4; ++r) {
       const int k = tk + 2 * (r & 1) + 16 * (r >> 1), x = 2 * (r & 1);
       const float ks = sc[k], vs = fmaxf(sc[kKaTile + k], kKvMinScale);
-      const float lv = fast_log2(vs);
-      isv[r] = __fdividef(C::kHalf ? kDown : 1.f, vs);
+      lv[r] = fast_log2(vs) + C::kUp;
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i) {
         const uint32_t(*p)[4] = s[r >> 1] + (HPW == 4 ? 0 : (i >> 1) * C::kParts);
@@ -644,12 +654,12 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
           const uint32_t p1 = HPW == 4 ? p[0][x + 1] : p[1][x + (i & 1)], p2 = HPW == 4 ? p[1][x] : p[C::kParts - 1][x + (i & 1)];
           z = fmaf(static_cast<float>(static_cast<int>(p0) * 256 + static_cast<int>(p1)), 256.f, static_cast<float>(static_cast<int>(p2)));
         }
-        w[r][i] = ks >= 0.f ? fmaf(z, qs[i] * ks, lv) : -INFINITY;  // u
+        w[r][i] = ks >= 0.f ? fmaf(z, qs[i] * ks, lv[r]) : -INFINITY;  // u
         over |= w[r][i] > m[i] + (kKaSlack + C::kUp);
       }
     }
     if (__any_sync(0xffffffffu, over)) {
-      since = 1;
+      since = 0;
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i) {
         float mx = fmaxf(fmaxf(w[0][i], w[1][i]), fmaxf(w[2][i], w[3][i]));
@@ -657,9 +667,10 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
         mx = fmaxf(mx - C::kUp, m[i]);
-        const float alpha = mx == -INFINITY ? 1.f : fast_exp2(m[i] - mx);
+        // in two halves: sums may be as large as alpha is small
+        const float half = mx == -INFINITY ? 1.f : fast_exp2((m[i] - mx) * 0.5f), alpha = half * half;
         m[i] = mx;
-        ls[i] = (ls[i] + l[i]) * alpha;
+        ls[i] = (ls[i] + l[i]) * half * half;
         l[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
@@ -692,9 +703,30 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
     for (int i = 0; i < C::kHL; ++i) {
       const float ref = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
+      for (int r = 0; r < 4; ++r) w[r][i] -= ref;
+    }
+    if constexpr (HPW == 16) {
+      bool far = false;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) far |= fabsf(lv[r]) > 29.f;  // log2 sv + 14
+      wide |= __any_sync(0xffffffffu, far) != 0;
+    }
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < C::kHL; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) l[i] += fast_exp2(w[r][i] - lv[r]);
+    }
+#pragma unroll
+    for (int i = 0; i < C::kHL; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) w[r][i] = fast_exp2(w[r][i]);
+    if (!wide) {
+#pragma unroll
       for (int r = 0; r < 4; ++r) {
-        w[r][i] = fast_exp2(w[r][i] - ref);
-        l[i] = fmaf(w[r][i], isv[r], l[i]);
+        const float isv = fast_exp2(-lv[r]);
+#pragma unroll
+        for (int i = 0; i < C::kHL; ++i) l[i] = fmaf(w[r][i], isv, l[i]);
       }
     }
 
