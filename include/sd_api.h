@@ -397,7 +397,7 @@ sd_status sd_kv_load(sd_kv_cache kv, const int32_t* tok_start, const int32_t* bl
  *            duplicates are attended as listed
  *   out      bf16 [B, H, D], 8-byte aligned; zero where nothing is attended
  *   lse      fp32 [B, H] or NULL: ln sum exp z, -inf where nothing is attended
- * H % G == 0, H / G <= 128, n_list * index_block < 2^30, fewer than 2^36 tokens (of whole listed
+ * n_list >= 1 with a list. H % G == 0, H / G <= 128, n_list * index_block < 2^30, fewer than 2^36 tokens (of whole listed
  * blocks) over all requests, pools below 64 GiB. Scales must be finite
  * and not negative (a V scale below 2^-100 counts as 2^-100). A token on a bad page is skipped and flags SD_DEVERR_PAGE.
  * Slots behind a request's last token may hold anything. Logits and sums are

@@ -615,6 +615,8 @@ def sd_kv_attn(q, cache: KvCache, block_table, seqlens, scale: float, indices=No
     n, ip = 0, None
     if indices is not None:
         n = indices.shape[-1]
+        if n < 1:  # an empty tensor has no address, and a call without one attends every token
+            raise ValueError("indices must list at least one entry per (request, KV head)")
         ip = _need(indices, "indices", torch.int32, (B, G, n), dev)
     ws, ws_bytes = _workspace(workspace, 0 if workspace is not None else lib.sd_kv_attn_workspace_size(B, G, H, D), cache,
                               stream)
