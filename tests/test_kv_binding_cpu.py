@@ -43,3 +43,32 @@ def test_a_list_without_entries_is_refused(fake):
     sd.sd_kv_attn(q, cache, table, lens, 0.1)
     (_, listed), (_, every) = lib.calls
     assert listed[4] and listed[5] == 1 and every[4] is None
+
+
+@pytest.mark.parametrize("call", ["sd_kv_attn", "sd_block_topk", "sd_kv_block_step"])
+def test_the_default_workspace_lives_until_the_call_is_enqueued(fake, call):
+    """Freed earlier, its memory could be handed to another thread's tensor
+    before this call's kernels are in the stream."""
+    import gc
+    import weakref
+    cache, lib = fake
+    made, seen = [], []
+    empty = cache._empty
+
+    def recorded(shape, dtype, stream):
+        t = empty(shape, dtype, stream)
+        if dtype is torch.uint8:
+            made.append(weakref.ref(t))
+        return t
+
+    def enter(*args):
+        gc.collect()
+        t = made[0]()
+        seen.append(t is not None and (t.data_ptr(), t.nbytes) == (args[-2], args[-1]))
+
+    cache._empty = recorded
+    setattr(lib, call, enter)
+    q, table, lens = _inputs()
+    args = {"sd_kv_attn": (0.1,), "sd_block_topk": (2, 20), "sd_kv_block_step": (2, 20, 0.1)}[call]
+    getattr(sd, call)(q, cache, table, lens, *args)
+    assert len(made) == 1 and seen == [True]

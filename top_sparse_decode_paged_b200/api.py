@@ -594,12 +594,15 @@ def alloc_block_step_workspace(B: int, G: int, H: int, D: int, max_seqlen: int, 
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device or "cuda")
 
 
-def _workspace(workspace, nbytes: int, cache: KvCache, stream):
+def _workspace(workspace, nbytes: int, cache: KvCache, stream) -> torch.Tensor:
+    """The caller's workspace, or a new one. Callers hold it until the library
+    has enqueued the call: freed before, its memory may go to another thread's
+    tensor whose kernel runs first."""
     if workspace is None:
         workspace = cache._empty((max(nbytes, 1),), torch.uint8, stream)
     if workspace.get_device() != cache._dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {cache.device}")
-    return workspace.data_ptr(), workspace.nbytes
+    return workspace
 
 
 def sd_kv_attn(q, cache: KvCache, block_table, seqlens, scale: float, indices=None, index_block: int = 1, out=None,
@@ -618,13 +621,13 @@ def sd_kv_attn(q, cache: KvCache, block_table, seqlens, scale: float, indices=No
         if n < 1:  # an empty tensor has no address, and a call without one attends every token
             raise ValueError("indices must list at least one entry per (request, KV head)")
         ip = _need(indices, "indices", torch.int32, (B, G, n), dev)
-    ws, ws_bytes = _workspace(workspace, 0 if workspace is not None else lib.sd_kv_attn_workspace_size(B, G, H, D), cache,
+    workspace = _workspace(workspace, 0 if workspace is not None else lib.sd_kv_attn_workspace_size(B, G, H, D), cache,
                               stream)
     bt, pd = cache._paged(block_table, B)
     cache._call(stream, lib.sd_kv_attn, _need(q, "q", torch.bfloat16, (B, H, D), dev), cache._kv, bt,
                 _need(seqlens, "seqlens", torch.int32, (B,), dev), ip, n, index_block, pd, B, H, scale,
                 _need(out, "out", torch.bfloat16, (B, H, D), dev),
-                None if lse is None else _need(lse, "lse", torch.float32, (B, H), dev), ws, ws_bytes)
+                None if lse is None else _need(lse, "lse", torch.float32, (B, H), dev), workspace.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -638,12 +641,12 @@ def sd_block_topk(q, cache: KvCache, block_table, seqlens, n_select: int, max_se
     G, D, dev = cache.G, cache.D, cache._dev
     if indices is None:
         indices = cache._empty((B, G, n_select), torch.int32, stream)
-    ws, ws_bytes = _workspace(workspace, 0 if workspace is not None else
+    workspace = _workspace(workspace, 0 if workspace is not None else
                               lib.sd_block_topk_workspace_size(B, G, max_seqlen, cache.block_tokens), cache, stream)
     bt, pd = cache._paged(block_table, B)
     cache._call(stream, lib.sd_block_topk, _need(q, "q", torch.bfloat16, (B, H, D), dev), cache._kv, bt,
                 _need(seqlens, "seqlens", torch.int32, (B,), dev), pd, B, H, max_seqlen, n_select, n_first, n_last,
-                _need(indices, "indices", torch.int32, (B, G, n_select), dev), ws, ws_bytes)
+                _need(indices, "indices", torch.int32, (B, G, n_select), dev), workspace.data_ptr(), workspace.nbytes)
     return indices
 
 
@@ -658,14 +661,14 @@ def sd_kv_block_step(q, cache: KvCache, block_table, seqlens, n_select: int, max
         indices = cache._empty((B, G, n_select), torch.int32, stream)
     if out is None:
         out = cache._empty((B, H, D), torch.bfloat16, stream)
-    ws, ws_bytes = _workspace(workspace, 0 if workspace is not None else
+    workspace = _workspace(workspace, 0 if workspace is not None else
                               lib.sd_kv_block_step_workspace_size(B, G, H, D, max_seqlen, cache.block_tokens), cache, stream)
     bt, pd = cache._paged(block_table, B)
     cache._call(stream, lib.sd_kv_block_step, _need(q, "q", torch.bfloat16, (B, H, D), dev), cache._kv, bt,
                 _need(seqlens, "seqlens", torch.int32, (B,), dev), pd, B, H, max_seqlen, n_select, n_first, n_last, scale,
                 _need(indices, "indices", torch.int32, (B, G, n_select), dev),
                 _need(out, "out", torch.bfloat16, (B, H, D), dev),
-                None if lse is None else _need(lse, "lse", torch.float32, (B, H), dev), ws, ws_bytes)
+                None if lse is None else _need(lse, "lse", torch.float32, (B, H), dev), workspace.data_ptr(), workspace.nbytes)
     return indices, out
 
 
