@@ -20,6 +20,7 @@
 #include "kv_attn.cuh"
 #include "kv_store.cuh"
 #include "sd_common.cuh"
+#include "smem_limit.h"
 #include "sparse_index.cuh"
 #include "topk_cluster.cuh"
 #include "topk_radix.cuh"
@@ -58,29 +59,16 @@ sd_status cuda_check(cudaError_t e) {
   return SD_ERR_CUDA;
 }
 
-// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (device, kernel,
-// size): the attribute outlives the call, and setting it on every launch
-// costs host time on the decode loop.
+// Raises the kernel's dynamic shared memory limit on the current device to `bytes` where it is lower.
 sd_status set_smem_limit(const void* kern, size_t bytes) {
-  struct Entry { const void* k; int dev; size_t bytes; };
-  static std::mutex mu;
-  static Entry done[64];
-  static int n_done = 0;
+  static sd::SmemLimits limits;
   int dev = 0;
-  sd_status s = cuda_check(cudaGetDevice(&dev));
+  const sd_status s = cuda_check(cudaGetDevice(&dev));
   if (s != SD_OK) return s;
-  std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < n_done; ++i)
-    if (done[i].k == kern && done[i].dev == dev && done[i].bytes >= bytes) return SD_OK;
-  s = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)));
-  if (s != SD_OK) return s;
-  for (int i = 0; i < n_done; ++i)
-    if (done[i].k == kern && done[i].dev == dev) {
-      done[i].bytes = bytes;
-      return SD_OK;
-    }
-  if (n_done < 64) done[n_done++] = Entry{kern, dev, bytes};
-  return SD_OK;
+  const int e = limits.raise(kern, dev, bytes, [&](size_t n) {
+    return static_cast<int>(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(n)));
+  });
+  return e == sd::SmemLimits::kNoRoom ? SD_ERR_UNSUPPORTED : cuda_check(static_cast<cudaError_t>(e));
 }
 
 sd_status after_launch() {
