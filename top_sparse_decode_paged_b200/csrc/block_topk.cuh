@@ -26,10 +26,14 @@
 // matrix instructions give 16 blocks x 8 heads at a time to within a bound
 // that they sum as well (sum_d |q_d| max(|lo_d|, |hi_d|), times 2^-14): blocks
 // further than twice that from the border are settled, and the others, five
-// of 1024 for normal values, get their exact scores. Where the bound does not hold (values that are not finite,
-// or so large or small that a product leaves fp32's range) or over 256 blocks are too close, the
-// row is scored exactly, by the one CTA that selects (128 rows of 1024 equal
-// blocks: 72 us a call, of 4096: 262 us).
+// of 1024 for normal values, get their exact scores. The border is found by a
+// histogram over the scores' leading bits, refined while a digit holds more
+// blocks than are worth scoring (unrefined, rows around a power of two, around
+// zero or with one block on a bad page listed hundreds: 128 rows of 1024
+// around 2.0 took 72 us, now 19). Where the bound does not hold (values that
+// are not finite, or so large or small that a product leaves fp32's range) or
+// over 256 blocks lie within it of the border, the row is scored exactly, by
+// the one CTA that selects (128 rows of 1024 equal blocks: 72 us a call, of 4096: 262 us).
 //
 // Split of the selection: rows of up to kBsMaxBlocks blocks are scored and
 // selected in one launch by a cluster per (request, KV head), whose CTAs send
@@ -255,9 +259,11 @@ __device__ __forceinline__ uint32_t bf16x2_pick(uint32_t x, uint32_t y) {
 // . min(q, 0), 16 blocks x 8 heads at a time. Returns, as fp32 bits, the largest sum_d
 // |q_d| max(|lo_d|, |hi_d|) or score met; infinity (or NaN, above that) where
 // the error has no such bound. The error: a product of two bf16 values is exact in fp32, and
-// an instruction aligns its 17 addends to the largest and cuts each at 2^-23
-// of it at worst, as the sum; 2 D / 16 = 16 instructions make 288 * 2^-23 <
-// 2^-14.8 of the terms' sum.
+// an instruction is taken to align its 17 addends to the largest and to cut
+// each, and the sum, at 2^-23 of it at worst; 2 D / 16 = 16 instructions make
+// 288 * 2^-23 < 2^-14.8 of the terms' sum. (How it rounds is not documented;
+// over 10^8 scores of normal, wide-ranging and cancelling values the
+// worst error was 2^-19.2.)
 template <int D, class Ready>
 __device__ __forceinline__ uint32_t approx_blocks(const BlockScoreArgs& a, int b, int g, int c0, int len, int count,
                                                   unsigned char* ring, int32_t* keys, Ready ready) {
@@ -415,7 +421,7 @@ struct alignas(16) BlockSelectSmem {  // the rings, copied to in 16-byte pieces,
   int where[kBsList];
   uint32_t mag;
   int sure;
-  int n, digit, above, take;
+  int n, digit, above, inside, take;
   uint32_t key;
   int cnt[kBsPer * kWarps];
   float best[kWarps][32];
@@ -493,7 +499,7 @@ __device__ __forceinline__ bool select_blocks(BlockSelectSmem& sm, int count, in
       if (above < want && above + own >= want) {
 #pragma unroll
         for (int j = kBinsPer - 1; j >= 0; --j) {
-          if (above < want && above + static_cast<int>(h[j]) >= want) sm.digit = tid * kBinsPer + j, sm.above = above;
+          if (above < want && above + static_cast<int>(h[j]) >= want) sm.digit = tid * kBinsPer + j, sm.above = above, sm.inside = static_cast<int>(h[j]);
           above += h[j];
         }
       }
@@ -511,6 +517,9 @@ __device__ __forceinline__ bool select_blocks(BlockSelectSmem& sm, int count, in
         const uint32_t d_lo = max(mn, top == 32 ? 0u : prefix << top), d_hi = min(mx, d_lo | ((1u << top) - 1u));
         const float mag = __uint_as_float(sm.mag), gap = mag * 2.5f / 16384.f;
         if (!(mag >= 9.094947e-13f && mag < 1.2676506e30f)) return false;  // 2^-40 (see `odd`), 2^100
+        // A digit is as wide as the row's exponents make it: an eighth of the score where the
+        // row straddles a power of two. One more round costs as much as two exact scores a warp.
+        if (top > 0 && sm.inside > 2 * kWarps && score_of(d_hi) - score_of(d_lo) > gap) continue;
         const float lo = score_of(d_lo) - gap, hi = score_of(d_hi) + gap;
         int above = 0;
         each([&](int c, uint32_t k) {
