@@ -153,7 +153,8 @@ sd_status sd_sparse_attn(const uint16_t* q, const uint16_t* k_pages, const uint1
  * score the maximum over KV heads. The `budget` largest are kept (ties to the
  * lower position), followed by the recent tail. The kept set is a top-budget
  * set of the exact scores up to the fp32 rounding of the sums. Pages past the new
- * lengths are free for the caller to release; the block table is unchanged.
+ * lengths are free for the caller to release; the block table is unchanged. If
+ * the pools are an sd_kv_cache's, its k_bounds are stale afterwards (see there).
  * max_seqlen is a host upper bound of seqlens (it sizes the workspace);
  * larger lengths are clamped and flag SD_DEVERR_SEQLEN.
  * Limits: D in {64, 128}; H / G in {1, 2, 4, 8}; H <= 256;
@@ -319,9 +320,14 @@ sd_status sd_indexer_topk_noalloc(const int8_t* qi, const int32_t* w, const int8
  * one fp32 scale per (block, KV head): the value of a code is code * scale.
  * k_bounds holds the smallest and the largest key of every block, KV head and
  * dim, for the selection of blocks; it may be NULL where nothing is selected.
- * Its entries, like the scales, stand for the tokens that the block holds.
+ * Its entries, like the scales, stand for the tokens that the block holds; the
+ * keys are those before coding, as bf16. What moves or overwrites K rows other than
+ * sd_kv_store leaves the bounds behind: after sd_tri_compact on bf16 pools
+ * they are rebuilt by sd_kv_load of all kept tokens and sd_kv_store of those
+ * rows as they are (no q, no weights, rot_dim 0).
  * D in {64, 128}, block_tokens <= 128, num_pages * page_size < 2^31 and
- * max_pages_per_req * page_size < 2^30; pools and bounds 16-byte aligned
+ * max_pages_per_req * page_size < 2^30 (SD_ERR_UNSUPPORTED otherwise);
+ * block_tokens divides page_size, pools and bounds 16-byte aligned
  * (SD_ERR_INVALID_ARG otherwise). (No counterpart on the pages: they read
  * caches that a serving stack has written.) */
 typedef enum sd_kv_type { SD_KV_BF16 = 0, SD_KV_INT8 = 1, SD_KV_E4M3 = 2 } sd_kv_type;
@@ -346,8 +352,8 @@ typedef struct sd_kv_cache {
  *               q_stride, k_stride, v_stride elements apart (a packed q, k, v
  *               projection is read in place); 8-byte aligned, strides
  *               multiples of 4. q may be NULL (only K and V are stored)
- *   tok_start   int32 [B + 1], ascending from 0; rows at or behind
- *               tok_start[B] are not read, and their q_out rows stay as they were
+ *   tok_start   int32 [B + 1], ascending from 0; what rows at or behind
+ *               tok_start[B] hold has no effect, and their q_out rows stay as they were
  *   positions   int32 [n_tokens]: the position each row is rotated to, or NULL:
  *               its position in the cache
  *   q_weight, k_weight  bf16 [D] or NULL (no norm): x * rsqrt(mean(x^2) + eps) * weight
@@ -357,7 +363,8 @@ typedef struct sd_kv_cache {
  *               none, inv_freq may be NULL), in pairs (i, i + rot_dim / 2), or
  *               (2i, 2i + 1) with interleaved != 0
  *   q_out       bf16 [n_tokens, H, D], 8-byte aligned; may be q where q is dense
- * Arithmetic is fp32, angles fp64; q_out and bf16 pools are rounded once. In
+ * Arithmetic is fp32; angles are 64-bit fractions of a turn, as exact as fp64
+ * products (2^-24 turns at position 2^30). q_out and bf16 pools are rounded once. In
  * an 8-bit pool the scale of a (block, KV head) is
  *   max(amax(new rows) / qmax, the scale it had if it holds earlier tokens, 2^-100)
  * (qmax 127 or 448), codes are round(y / scale) of the fp32 quotient, ties to
@@ -416,8 +423,11 @@ sd_status sd_kv_attn(const uint16_t* q, sd_kv_cache kv, const int32_t* block_tab
 /* Selection of blocks by a bound on their scores (any kv_type; kv.k_bounds is
  * read, the pools are not): block c of KV head g scores
  *   max over the group's query heads of sum_d max(q_d * lo_d, q_d * hi_d)
- * summed in fp64 and rounded to fp32, at least the largest q . k of the block
- * (a head whose sum is not a number is left out; the bounds are finite).
+ * summed in fp64 and rounded to fp32: at least the largest q . k of the block's
+ * keys as they were before coding. (The coded keys of an 8-bit pool may lie outside
+ * the bounds by what coding them cost: half a scale in int8, 2^-4 of the
+ * value in e4m3, as much again each time the block's scale grew.) A head
+ * whose sum is not a number is left out; the bounds are finite.
  *   q        bf16 [B, H, D], 8-byte aligned
  *   indices  int32 [B, G, n_select]  OUT: the first n_first and the last n_last
  *            blocks of the request and the best others, min(n_select, number
@@ -425,8 +435,9 @@ sd_status sd_kv_attn(const uint16_t* q, sd_kv_cache kv, const int32_t* block_tab
  * 1 <= n_select <= 2048, n_first + n_last <= n_select, max_seqlen <= 2^20 *
  * block_tokens, B * G <= 65535, H / G <= 128. A block on a bad page scores -inf and
  * flags SD_DEVERR_PAGE. max_seqlen is a host upper bound of seqlens.
- * The indices fit sd_kv_attn with index_block = block_tokens, and
- * sd_sparse_attn_csr with offsets r * n_select and block_size = block_tokens.
+ * The indices fit sd_kv_attn with index_block = block_tokens, and, on bf16
+ * pools, sd_sparse_attn_csr with offsets r * n_select and block_size =
+ * block_tokens, while n_select * block_tokens is within its limit of a row.
  * Workspace: sd_block_topk_workspace_size(). */
 size_t sd_block_topk_workspace_size(int32_t B, int32_t G, int32_t max_seqlen, int32_t block_tokens);
 sd_status sd_block_topk(const uint16_t* q, sd_kv_cache kv, const int32_t* block_table, const int32_t* seqlens,

@@ -444,7 +444,10 @@ class KvCache:
     slots, fp32 scales ``[num_pages, page_size // block_tokens, G]`` of 8-bit
     pools and, where blocks are selected, the bf16 bounds of every block's
     keys ``[num_pages, page_size // block_tokens, G, 2, D]`` (lo, hi). Holds
-    the tensors; the library reads and writes them in place."""
+    the tensors; the library reads and writes them in place. ``sd_tri_compact``
+    on the pools leaves the bounds stale: read the kept tokens with
+    ``sd_kv_load`` and store them again as they are (``q`` and ``inv_freq``
+    None) to rebuild them."""
 
     def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None, k_bounds=None, block_tokens: Optional[int] = None):
         if k_pages.dim() != 4 or k_pages.dtype not in _KV_TYPES:
@@ -634,7 +637,7 @@ def sd_kv_attn(q, cache: KvCache, block_table, seqlens, scale: float, indices=No
 def sd_block_topk(q, cache: KvCache, block_table, seqlens, n_select: int, max_seqlen: int, n_first: int = 1,
                   n_last: int = 1, indices=None, workspace=None, stream=None):
     """The blocks of each (request, KV head) with the largest bound on their
-    scores, the first ``n_first`` and last ``n_last`` always among them.
+    scores (of the keys before coding), the first ``n_first`` and last ``n_last`` always among them.
     Returns ``indices`` [B, G, n_select] int32, ascending, -1 padded."""
     lib = load_library()
     B, H = q.shape[0], q.shape[1]
