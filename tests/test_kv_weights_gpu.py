@@ -122,3 +122,28 @@ def test_zero_values_beside_large_ones(kind, qpk, G, first, sv, zero):
     got, want = f64(out), 0.5 * c * sv
     assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -14) * want).all(), (got.min() / want, got.max() / want)
     assert (np.abs(f64(lse) - np.log(2 * (L - 1))) <= 2.0 ** -14).all(), f64(lse).ravel()[:4]
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("qpk", [1, 5, 16])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 22, 2.0 ** 23, 2.0 ** 24, 2.0 ** 25, 2.0 ** 26, 2.0 ** 27, 2.0 ** 28, 2.0 ** 40])
+def test_logits_whose_last_place_is_above_one(kind, qpk, size):
+    """Every token has the same V, so the output is V (its rounding 2^-8, weights and
+    sums 2^-10) whatever the logits are: rising and falling ones that differ by
+    single units in the last place of fp32, and by more."""
+    import torch
+    import top_sparse_decode_paged_b200 as sd
+    rng = np.random.default_rng(int(np.log2(size)))
+    D, P, L, G = 64, 16, 16 * 148, 4
+    c = CODE[kind]
+    k = np.zeros((L // P, P, G, D), np.float32)
+    k[..., 0] = 1
+    steps = rng.integers(-3, 4, (L, G)).cumsum(0) + rng.integers(0, 30, (L, G)) * (rng.random((L, G)) < 0.2)
+    ks = (np.float32(size) + steps * np.spacing(np.float32(size))).astype(np.float32)
+    v = np.full((L // P, P, G, D), c, np.float32)
+    cache = sd.KvCache(_pool(k, kind), _pool(v, kind), torch.from_numpy(ks).cuda().view(L // P, P, G),
+                       torch.ones((L // P, P, G), device="cuda"), None, 1)
+    table = torch.arange(L // P, dtype=torch.int32)[None].cuda()
+    for scale in (float(np.log(2)), 1.0, 3.7):
+        out = f64(sd.sd_kv_attn(_first_dim_queries(1, G * qpk, D), cache, table, torch.tensor([L], dtype=torch.int32).cuda(), scale))
+        assert (np.abs(out - c) <= (2.0 ** -8 + 2.0 ** -10) * c).all(), (scale, out.min(), out.max())

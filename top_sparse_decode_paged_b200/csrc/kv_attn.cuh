@@ -421,7 +421,10 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
   // 2^-15. (Groups of up to 8 heads always take it themselves, at no cost; with
   // 16 heads each, 128 query heads 186 us so and 200 always, in e4m3.)
   bool wide = HPW != 16;
-  float m[C::kHL];                // log2 of what a weight of 1 stands for: M - kUp
+  // log2 of what a weight of 1 stands for: M - kUp, rounded up, and weights
+  // pass it by slack + kUp, rounded down, so that none leaves its range where logits
+  // are so large that their last place is above one
+  float m[C::kHL];
   float l[C::kHL], ls[C::kHL];    // sums of weights: the last tiles', and those before
   uint32_t o[C::kOTiles][D / 16][4] = {};  // int32 or fp32 sums; D / 16 tiles of 16 dims
   constexpr bool kFold = !C::kHalf;  // int32 sums
@@ -655,7 +658,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
           z = fmaf(static_cast<float>(static_cast<int>(p0) * 256 + static_cast<int>(p1)), 256.f, static_cast<float>(static_cast<int>(p2)));
         }
         w[r][i] = ks >= 0.f ? fmaf(z, qs[i] * ks, lv[r]) : -INFINITY;  // u
-        over |= w[r][i] > m[i] + (kKaSlack + C::kUp);
+        over |= w[r][i] > __fadd_rd(m[i], kKaSlack + C::kUp);
       }
     }
     if (__any_sync(0xffffffffu, over)) {
@@ -666,7 +669,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        mx = fmaxf(mx - C::kUp, m[i]);
+        mx = fmaxf(__fadd_ru(mx, -C::kUp), m[i]);
         // in two halves: sums may be as large as alpha is small
         const float half = mx == -INFINITY ? 1.f : fast_exp2((m[i] - mx) * 0.5f), alpha = half * half;
         m[i] = mx;
