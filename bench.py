@@ -39,13 +39,12 @@ L2_FLUSH_BYTES = 256 << 20
 # DRAM traffic (dram__bytes_read.sum + dram__bytes_write.sum) of one launch,
 # from the ncu captures summarised in profiles/, keyed by (workload, stage).
 # Valid only for the library version they were taken on; any other version
-# reports traffic as null. (Captured on version 7; version 8 adds calls and
-# leaves these two kernels as they were.)
+# reports traffic as null.
 NCU_TRAFFIC = {
     # captured at --batch 16 (half the workload's 32 requests) and scaled by 2:
     # both kernels' traffic grows with the requests they process
-    ("b32_l65536_mla", "indexer"): (0x00000008, 2 * (134.464000e6 + 4.018176e6)),
-    ("b32_l65536_mla", "attn"): (0x00000008, 2 * (40.339456e6 + 1.273856e6)),
+    ("b32_l65536_mla", "indexer"): (0x00000008, 2 * (134.466816e6 + 3.613696e6)),
+    ("b32_l65536_mla", "attn"): (0x00000008, 2 * (40.347136e6 + 0.592640e6)),
 }
 
 

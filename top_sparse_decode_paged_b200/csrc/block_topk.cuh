@@ -1,17 +1,19 @@
 // Selection of cache blocks by a bound on their scores: for query head h and
 // block c of KV head g with per-dim bounds lo, hi of the block's keys,
-//   q . k <= sum_d max(q_d lo_d, q_d hi_d)   for every key k of the block,
-// and a block's score is the largest bound over the group's query heads. The
-// first n_first and last n_last blocks of a request are always kept; the
-// library's top-k takes the best others, ties to the lower block.
+//   q . k <= sum_d max(q_d lo_d, q_d hi_d)   for every key k of the block
+// (as it was before coding), and a block's score is the largest bound over the
+// group's query heads. The first n_first and last n_last blocks of a request
+// are always kept; the library's top-k takes the best others, ties to the lower
+// block.
 //
 // The sums are held in fp64, where a product of two bf16 values is exact and
-// the sum is wrong by 2^-46 of its terms at most, and rounded once to fp32:
-// which blocks are selected does not depend on the order of the sum.
-// max(q lo, q hi) is q times one of the two, picked by q's sign. A bf16 value
-// becomes a double by moving its bits: (x >> 3) with the sign kept, as the
-// high word, is x * 2^-896 for every finite x, subnormals and zero included;
-// q carries 2^800 and the result 2^96 to make up for it.
+// the sum is wrong by 2^-46 of its terms at most, and rounded once to fp32: the
+// order of the sum matters only to a score that lies that close to the middle
+// of two fp32 numbers, and a row is ranked by scores of one order. max(q lo, q
+// hi) is q times one of the two, picked by q's sign. A bf16 value becomes a
+// double by moving its bits: (x >> 3) with the sign kept, as the high word, is
+// x * 2^-896 for every finite x, subnormals and zero included; q carries 2^800
+// and the result 2^96 to make up for it.
 //
 // Split of the exact scores: D / 4 lanes share a block, four dims each, so that a
 // lane keeps its dims of four query heads in registers; the bounds stream
@@ -432,12 +434,12 @@ constexpr size_t kBsSmem = sizeof(BlockSelectSmem) + (size_t)(kBsThreads / 32) *
 // The n largest of sm.keys[0 .. count), count > n, ties to the lower index,
 // written ascending, by one CTA; sm.hist is zero, sm.n and sm.sure 0. APPROX:
 // the keys are within sm.mag * 2^-14 of the scores. The digit of the last key
-// to take then bounds the last score to take to within twice that; blocks
-// above are taken, blocks below left, and `rescore` makes exact keys of those
-// between for the list to be ranked by. False: too many lie between, or the
-// error has no bound (the histogram is zero again). Loops stay rolled here and in the scores: these
-// kernels run between others that stream the cache, and fetching their code
-// anew cost more than their arithmetic.
+// to take then bounds the last score to take to within twice that; blocks above
+// are taken, blocks below left, and `rescore` makes exact keys of those between
+// for the list to be ranked by. False: too many lie between, or the error has
+// no bound (the histogram is zero again). Loops stay rolled here and in the
+// scores: these kernels run between others that stream the cache, and fetching
+// their code anew cost more than their arithmetic.
 template <bool APPROX, class Locate, class Rescore>
 __device__ __forceinline__ bool select_blocks(BlockSelectSmem& sm, int count, int n, int32_t* out, Locate locate, Rescore rescore) {
   constexpr int kWarps = kBsThreads / 32;

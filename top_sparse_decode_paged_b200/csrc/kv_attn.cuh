@@ -16,7 +16,7 @@
 // up to 8, with the fourth rounded into them by a sequence that goes evenly
 // over its range. (Rounded to the nearest, weights below 2^-24 were lost
 // altogether, and 2^18 of them beside a large one are a hundredth of the sum.
-// Four bytes for 8 heads: 64 query heads 192 us instead of 171.) (Unpacking
+// Four bytes for 8 heads: 64 query heads 192 us instead of 170.) (Unpacking
 // codes to fp16 instead took 80 to 140 integer instructions per 16 tokens, a
 // third of the loop.) e4m3: the 8-bit instruction takes as long as two fp16
 // ones after a conversion that it repeats for every part, so codes are
@@ -56,10 +56,11 @@
 // writes one partial (O, M, l) for each of them, and a combine merges the
 // partials in closed form from the list. Ragged batches need no host
 // schedule. Bound by HBM where there is enough to read: 2 D bytes per token
-// and KV head. 32 query heads over 8 KV heads of 128: 16 x 32768 tokens (1075 MB) in
-// 163.3 us, 6.58 TB/s, the rate of a plain copy, in either type (64 query
-// heads 171 us int8 and 166 e4m3, 128 heads 226 and 186); 16
-// requests of 1040 to 9232 tokens (127 MB, e4m3) 28.2 us; 1000 tokens 7.8 us, launches and trips to memory.
+// and KV head. 32 query heads over 8 KV heads of 128: 16 x 32768 tokens (1075
+// MB) in 163.4 us, 6.58 TB/s, the rate of a plain copy, in either type (64
+// query heads 170 us int8 and 166 e4m3, 128 heads 226 and 186); 16 requests of
+// 1040 to 9232 tokens (127 MB, e4m3) 28.5 us; 1000 tokens 7.9 us, launches and
+// trips to memory.
 #pragma once
 
 #include "kv_store.cuh"

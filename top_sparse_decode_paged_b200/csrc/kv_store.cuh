@@ -7,11 +7,13 @@
 //   over the pairs (i, i + R/2), or (2i, 2i + 1), of the first R dims.
 // The angle is taken in turns, with the frequency as a 64-bit fixed-point
 // fraction of a turn: position times frequency modulo one turn is an integer
-// product modulo 2^64, exact to 2^-34 turns at any 32-bit position, where a
-// far position times a frequency in fp32 keeps only a few bits of its fraction. q is rounded once to bf16. K and V go into a bf16,
-// int8 or e4m3 pool. An 8-bit pool is cut into blocks of `bs` consecutive
-// slots (a page holds whole blocks); a block and KV head have one scale for K
-// and one for V:
+// product modulo 2^64. The frequency comes from an fp64 product, off by 2^-54
+// turns at a frequency of one radian, so the angle is as exact as one in fp64
+// (2^-24 turns at position 2^30), where a far position times a frequency in
+// fp32 keeps only a few bits of its fraction. q is rounded once to bf16. K and
+// V go into a bf16, int8 or e4m3 pool. An 8-bit pool is cut into blocks of `bs`
+// consecutive slots (a page holds whole blocks); a block and KV head have one
+// scale for K and one for V:
 //   s = max(amax(new rows) / qmax, s of the block's earlier rows, 2^-100)
 // with qmax 127 or 448, codes round(y / s), and the earlier rows of a block
 // whose scale grew coded anew, round(code * (s_old / s_new)). A growing scale
@@ -24,13 +26,14 @@
 // Work split, one launch. K and V: the scale needs all of a block's new rows
 // before any is coded. A prompt gets one CTA per (touched block, KV head),
 // which keeps the rotated rows in shared memory in between; a decode step one
-// warp per (token, KV head), K in one part of its lanes and V in the other,
-// and units of several rows fall back to the whole CTA. q: one group of D / 8 lanes per (token,
-// group of heads); the token's angles are computed once per group and used
-// for its heads. 32 query heads over 8 KV heads of 128: four prompts into int8
-// (212 MB of q, 40 M instructions) 64 us, bound by issue slots (65 % used) and
-// then HBM; three prompts into bf16 32.8 us; one token 3.7 us and 64 tokens
-// 4.6 us, bound by launch and load latency.
+// warp per (token, KV head), K in one part of its lanes and V in the other, and
+// units of several rows fall back to the whole CTA. q: one group of D / 8 lanes
+// per (token, group of heads); the token's angles are computed once per group
+// and used for its heads. 32 query heads over 8 KV heads of 128: four prompts
+// into int8 (212 MB of q, 42.5 M instructions) 63.7 us, three prompts into bf16
+// 32.8 us, bound by the chains of dependent steps at 24 warps per SM (issue
+// slots 66 and 62 % used, HBM 37 % in int8, waits for loads the first stall);
+// one token 3.7 us and 64 tokens 4.6 us, bound by launch and load latency.
 #pragma once
 
 #include <float.h>
@@ -789,8 +792,9 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv_store_kernel(const __grid_co
 
 // Reads the tokens that a store with the same tok_start and seqlens wrote back
 // as bf16 rows [T, G, D]: code * scale, rounded once. One warp per token, a
-// 16-element piece per lane and step. Bound by HBM: the four prompts' int8
-// rows in 14.6 us.
+// 16-element piece per lane and step. The four prompts' int8 rows (65.8 MB) in
+// 14.5 us after the store, 17.0 with cold caches, bound by each warp's chain
+// page, scale, codes.
 struct KvLoadArgs {
   const void *k_pages, *v_pages;
   const float *k_scales, *v_scales;
