@@ -147,3 +147,29 @@ def test_logits_whose_last_place_is_above_one(kind, qpk, size):
     for scale in (float(np.log(2)), 1.0, 3.7):
         out = f64(sd.sd_kv_attn(_first_dim_queries(1, G * qpk, D), cache, table, torch.tensor([L], dtype=torch.int32).cuda(), scale))
         assert (np.abs(out - c) <= (2.0 ** -8 + 2.0 ** -10) * c).all(), (scale, out.min(), out.max())
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("qpk", [1, 5, 16])
+@pytest.mark.parametrize("L", [31, 4736])
+@pytest.mark.parametrize("sv", [2.0 ** 120, 2.0 ** 90, 2.0 ** -60, 2.0 ** -100])
+def test_equal_values_near_the_ends_of_the_range(kind, qpk, L, sv):
+    """Every token has the same V, 100 times a scale that puts it near the largest
+    bf16 or far below one: the output is V (its rounding 2^-8, weights and sums 2^-10)."""
+    import torch
+    import top_sparse_decode_paged_b200 as sd
+    rng = np.random.default_rng(L)
+    D, P, G = 64, 16, 4
+    c, n = CODE[kind], -(-L // P)
+    k, v = np.zeros((n, P, G, D), np.float32), np.full((n, P, G, D), c, np.float32)
+    k[..., 0] = rng.integers(-30, 31, (n, P, G))
+    cache = sd.KvCache(_pool(k, kind), _pool(v, kind), torch.ones((n, 1, G), device="cuda"), torch.full((n, 1, G), sv, device="cuda"))
+    table = torch.arange(n, dtype=torch.int32)[None].cuda()
+    lse = torch.empty((1, G * qpk), device="cuda")
+    out = f64(sd.sd_kv_attn(_first_dim_queries(1, G * qpk, D), cache, table, torch.tensor([L], dtype=torch.int32).cuda(), 0.1, lse=lse))
+    want = c * sv
+    assert (np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -10) * want).all(), (out.min() / want, out.max() / want)
+    z = 0.1 * f64(cache.k_pages)[..., 0].reshape(-1, G)[:L]
+    ref = np.repeat(np.log(np.exp(z).sum(0)), qpk)
+    # logits of up to 20 + log2 sv in base 2, a few roundings of 2^-24 each
+    assert (np.abs(f64(lse)[0] - ref) <= 2.0 ** -14).all()

@@ -58,7 +58,7 @@
 // schedule. Bound by HBM where there is enough to read: 2 D bytes per token
 // and KV head. 32 query heads over 8 KV heads of 128: 16 x 32768 tokens (1075
 // MB) in 163.4 us, 6.58 TB/s, the rate of a plain copy, in either type (64
-// query heads 170 us int8 and 166 e4m3, 128 heads 226 and 186); 16 requests of
+// query heads 170 us int8 and 166 e4m3, 128 heads 228 and 186); 16 requests of
 // 1040 to 9232 tokens (127 MB, e4m3) 28.5 us; 1000 tokens 7.9 us, launches and
 // trips to memory.
 #pragma once
@@ -184,6 +184,12 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The same down to fp32's smallest number.
+__device__ __forceinline__ float fast_exp2_subnormal(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float fast_log2(float x) {
@@ -535,10 +541,11 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
       const int h = lane_head(i);
       if (h >= nh) continue;
       const size_t at = slot * a.H + h0 + h;
-      // V scales far from one leave s far from one: its power of two moves
-      // into M, by which the combine weighs partials
-      int e = s > 0.f && s < INFINITY ? min(static_cast<int>(__float_as_uint(s) >> 23), 253) - 127 : 0;
-      if (abs(e) <= 32) e = 0;
+      // V scales far from one leave s far from one: what its power of two has
+      // beyond 2^32 or below 2^-32 moves into M, by which the combine weighs
+      // partials (and no more, so that sums of large values stay in range)
+      const int pow = s > 0.f && s < INFINITY ? static_cast<int>(__float_as_uint(s) >> 23) - 127 : 0;
+      const int e = pow - max(-32, min(32, pow));
       const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       if (n == 0) a.part_ml[at] = make_float2(m[i] + static_cast<float>(e), s * f);
       float* dst = a.part_o + at * D + n;
@@ -719,7 +726,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
 #pragma unroll
       for (int i = 0; i < C::kHL; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) l[i] += fast_exp2(w[r][i] - lv[r]);
+        for (int r = 0; r < 4; ++r) l[i] += fast_exp2_subnormal(w[r][i] - lv[r]);  // 2^-121 where V is near the largest bf16
     }
 #pragma unroll
     for (int i = 0; i < C::kHL; ++i)
@@ -738,7 +745,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attn_kernel(const __grid_con
     // 4t .. 4t + 3 (+ 16), whose codes it holds ----
     if constexpr (!C::kHalf) {
       uint32_t pf[C::kOTiles][2];
-      const uint32_t weyl = kGolden * (at * kKaTile + tk);
+      const uint32_t weyl = kGolden * (static_cast<uint32_t>(at) * kKaTile + tk);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         uint32_t p[2][C::kHL];  // parts of rows n and n + 8

@@ -997,7 +997,7 @@ KvAttnPlan kv_attn_plan(int B, int G, int H, int D) {
   const int qpk = H / G;
   // Query heads that share a warp's K and V. 16 x 32768 tokens, 8 KV heads,
   // int8: 4 heads each in fours 163 us, in eights 165, in sixteens (fp16)
-  // 224; 16 heads each in sixteens 226, in eights (K and V read twice) 320.
+  // 224; 16 heads each in sixteens 228, in eights (K and V read twice) 320.
   p.hpw = qpk <= 4 ? 4 : qpk <= 8 ? 8 : 16;
   p.cols = G * sd::ceil_div(qpk, p.hpw);
   p.col_groups = sd::ceil_div(p.cols, sd::kKaWarps);
