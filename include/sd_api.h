@@ -404,14 +404,16 @@ sd_status sd_kv_load(sd_kv_cache kv, const int32_t* tok_start, const int32_t* bl
  *            duplicates are attended as listed
  *   out      bf16 [B, H, D], 8-byte aligned; zero where nothing is attended
  *   lse      fp32 [B, H] or NULL: ln sum exp z, -inf where nothing is attended
- * n_list >= 1 with a list. H % G == 0, H / G <= 128, n_list * index_block < 2^30, fewer than 2^36 tokens (of whole listed
- * blocks) over all requests, pools below 64 GiB. Scales must be finite
- * and not negative (a V scale below 2^-100 counts as 2^-100). A token on a bad page is skipped and flags SD_DEVERR_PAGE.
- * Slots behind a request's last token may hold anything. Logits and sums are
- * fp32; softmax weights, relative to the largest, are fixed point of 32 bits
- * (int8, H / G <= 4) or 24 (int8, H / G <= 8; what is cut is made up for over
- * neighbouring tokens), 22 bits of each weight (e4m3, H / G <= 8), or 11 bits
- * of each (H / G > 8).
+ * n_list >= 1 with a list. H % G == 0, H / G <= 128, n_list * index_block <
+ * 2^30, fewer than 2^36 tokens (of whole listed blocks) over all requests,
+ * pools below 64 GiB. Scales must be finite and not negative (a V scale below
+ * 2^-100 counts as 2^-100). A token on a bad page is skipped and flags
+ * SD_DEVERR_PAGE. Slots behind a request's last token may hold anything.
+ * Logits and sums are fp32, of queries rounded to 2^-22 (int8, H / G <= 8) or
+ * 2^-27 of their head's largest entry. Softmax weights, relative to the
+ * largest, are fixed point of 32 bits (int8, H / G <= 4) or 24 (int8, H / G
+ * <= 8; what is cut is made up for over neighbouring tokens); of their own
+ * bits they keep 22 (e4m3, H / G <= 8) or 11 (H / G > 8).
  * kv_type SD_KV_BF16 returns SD_ERR_UNSUPPORTED (sd_sparse_attn reads bf16 pools).
  * Workspace: sd_kv_attn_workspace_size(). */
 size_t sd_kv_attn_workspace_size(int32_t B, int32_t G, int32_t H, int32_t D);

@@ -6,25 +6,17 @@ import pytest
 
 pytestmark = pytest.mark.gpu
 
-D, G, BS = 128, 8, 32
+D, G, BS = 128, 8, 8
 
 
 def _cache(bounds):
-    """A cache for the selection, which reads bounds alone: the pools, which would be
-    gigabytes, have one page."""
+    """A cache with these bounds and pools of zeros, which the selection does not read."""
     import torch
     import top_sparse_decode_paged_b200 as sd
-
-    class Cache(sd.KvCache):
-        def __init__(self):
-            small = torch.zeros((1, BS, G, D), dtype=torch.int8, device="cuda")
-            one = torch.ones((1, 1, G), device="cuda")
-            super().__init__(small, small, one, one, None, BS)
-            self.num_pages = bounds.shape[0]
-            self.k_bounds = bounds.cuda()
-            self._kv.k_bounds = self.k_bounds.data_ptr()
-
-    return Cache()
+    N = bounds.shape[0]
+    pool = torch.zeros((N, BS, G, D), dtype=torch.int8, device="cuda")
+    scales = torch.ones((N, 1, G), device="cuda")
+    return sd.KvCache(pool, pool, scales, scales, bounds.cuda(), BS)
 
 
 def _case(scores, bad, seed):
